@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/moe.h"
+
 namespace moe {
 
 // Layer sizes in the notation of the DeepSeekMoE report: T tokens, hidden d, E = N_m routed
@@ -263,5 +265,24 @@ cudaError_t launch_balance(const Dims& D, float* z, const float* bias, const int
                            float* partial, float* psum, float* f, float* P, float* terms, cudaStream_t stream);
 // rows[r][col] = 1 and rows[r][col + 1 .. col + 63] = 0 (bf16), r < n_rows
 cudaError_t launch_fill_aug(void* rows, long long n_rows, int ld, int col, cudaStream_t stream);
+
+// ---- around the layer -------------------------------------------------------------------
+// RMS norm (norm.cu); fmt: moe_expert_fmt_t of the codes.  sum NULL iff res NULL, codes and scales
+// NULL iff fmt is MOE_FMT_NATIVE, rstd optional.
+constexpr int NORM_MAX_D = 16384;
+cudaError_t launch_rmsnorm(bool bf16, int fmt, const void* x, const void* res, const void* w, float eps, long long rows,
+                           int d, void* sum, void* y, uint8_t* codes, void* scales, float* rstd, cudaStream_t stream);
+// dx and dweight [d]; partial: norm_bwd_partials(rows) rows of d fp32.  dsum may be NULL.
+constexpr int NORM_BWD_BLOCKS = 296;
+int norm_bwd_partials(long long rows);
+cudaError_t launch_rmsnorm_bwd(bool bf16, const void* dy, const void* s, const void* w, const float* rstd, const void* dsum,
+                               long long rows, int d, void* dx, float* dweight, float* partial, cudaStream_t stream);
+// Norm of a list of tensors (grads.cu) and, with max_norm >= 0, the clipped tensors (in place, or to out).
+constexpr int GRAD_BLOCKS = 1024;             // partial sums in the workspace
+constexpr int GRAD_STATE_OFFSET = 16;         // in the workspace's first 256 bytes
+constexpr int GRAD_MAX_TENSORS = 65536, GRAD_MAX_LAUNCHES = 512;
+size_t grad_workspace_bytes();
+cudaError_t launch_grad_norm(const moe_tensor_t* t, const moe_tensor_t* out, int n, float max_norm, float* norm, void* ws,
+                             cudaStream_t stream);
 
 }  // namespace moe

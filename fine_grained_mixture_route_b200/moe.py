@@ -6,6 +6,7 @@ shared library is missing or the device is not a B200, calls raise.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, Optional
@@ -26,7 +27,8 @@ EXPORTED = ("moe_workspace_bytes", "moe_layer_launches", "moe_status_string", "m
             "moe_backward_workspace_bytes", "moe_layer_forward_train", "moe_layer_backward",
             "moe_layer_backward_timed", "moe_backward_launches", "moe_balance_workspace_bytes",
             "moe_balance_stats", "moe_gather_rows", "moe_segment_ids", "moe_selftest_wait_timeout",
-            "moe_mx_scale_bytes", "moe_quantize_weights_mx")
+            "moe_mx_scale_bytes", "moe_quantize_weights_mx", "moe_rmsnorm", "moe_rmsnorm_backward",
+            "moe_rmsnorm_backward_workspace_bytes", "moe_grad_workspace_bytes", "moe_grad_norm", "moe_clip_grads")
 NUM_STAGES = 7
 STAGE_NAMES = ("router", "permute", "plan", "gather", "gemm1_swiglu", "gemm2", "combine")
 BWD_STAGES = 7
@@ -45,6 +47,10 @@ class MoeWeights(ctypes.Structure):
 
 class MoeGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "b1", "w3", "b3", "w2", "b2")]
+
+
+class MoeTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -107,6 +113,18 @@ def _lib():
                                                 vp, vp, vp, vp]
         lib.moe_backward_launches.argtypes = [sh]
         lib.moe_backward_launches.restype = ctypes.c_int32
+        i32, i64, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+        lib.moe_rmsnorm.argtypes = [i32, i64, i32, vp, vp, vp, f32, vp, vp, i32, vp, vp, f32p, vp]
+        lib.moe_rmsnorm_backward_workspace_bytes.argtypes = [i32, i64, i32]
+        lib.moe_rmsnorm_backward_workspace_bytes.restype = sz
+        lib.moe_rmsnorm_backward.argtypes = [i32, i64, i32, vp, vp, vp, f32p, vp, vp, f32p, vp, sz, vp]
+        tp = ctypes.POINTER(MoeTensor)
+        lib.moe_grad_workspace_bytes.argtypes = []
+        lib.moe_grad_workspace_bytes.restype = sz
+        lib.moe_grad_norm.argtypes = [tp, i32, f32p, vp, sz, vp]
+        lib.moe_clip_grads.argtypes = [tp, tp, i32, f32, f32p, vp, sz, vp]
+        for n in ("moe_rmsnorm", "moe_rmsnorm_backward", "moe_grad_norm", "moe_clip_grads"):
+            getattr(lib, n).restype = ctypes.c_int
         for n in ("moe_check_device_error", "moe_ws_init", "moe_route", "moe_permute", "moe_expert_ffn",
                   "moe_combine", "moe_layer_forward", "moe_layer_forward_timed", "moe_quantize_rows_e4m3",
                   "moe_layer_forward_train", "moe_layer_backward", "moe_layer_backward_timed", "moe_balance_stats",
@@ -553,6 +571,194 @@ def selftest_wait_timeout(limit_ns: int, ws: torch.Tensor, out: Optional[torch.T
     _check(_lib().moe_selftest_wait_timeout(limit_ns, _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_selftest_wait_timeout")
     return out
+
+
+# ----------------------------------------------------------------------------- around the layer
+def _stream_of(dev: torch.device, stream=None):
+    """The given stream, else the current stream of the tensors' device (which need not be the current device)."""
+    return ctypes.c_void_p((torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream)
+
+
+_SAME_DEVICE = contextlib.nullcontext()
+
+
+def _device_of(dev: torch.device):
+    """Makes the tensors' device the current one for a call, where it is another."""
+    return _SAME_DEVICE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _rows(t, name: str, dtype=None, shape=None, device=None):
+    """A contiguous bf16 or fp32 matrix [rows, d] (the norm's inputs and outputs)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} has dtype {t.dtype}; {dtype or 'bfloat16 or float32'} is needed")
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous matrix [rows, d]")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; {tuple(shape)} is needed")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}; x is on {device}")
+
+
+def _exactly(t, name: str, shape, dtype, device):
+    """A contiguous tensor of this very shape, so that an output is filled as a whole."""
+    _need(t, name, 0, dtype, device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; {tuple(shape)} is needed")
+
+
+def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+            fmt: int = FMT_NATIVE, out: Optional[Dict] = None, stream=None) -> Dict:
+    """moe_rmsnorm: RMS norm of x [rows, d], or of x + residual.  Returns {"y", "sum" (the rounded x + residual, the
+    residual stream from here on; None without one), "rstd" (fp32 [rows], for the backward pass), "codes", "scale"}: with
+    fmt FMT_E4M3 uint8 codes [rows, d] and fp32 scales [rows], with FMT_MXFP8 codes and scale bytes
+    [rows, ceil(d / 32)] (layer_forward's x_quant), else None.  `out` may hold these tensors; out["sum"] may be
+    residual itself."""
+    _rows(x, "x")
+    rows, d = x.shape
+    dev, dt = x.device, x.dtype
+    _exactly(weight, "weight", (d,), dt, dev)
+    if residual is not None:
+        _rows(residual, "residual", dt, x.shape, dev)
+    if fmt not in (FMT_NATIVE, FMT_E4M3, FMT_MXFP8):
+        raise ValueError("fmt must be FMT_NATIVE, FMT_E4M3 or FMT_MXFP8")
+    want = {"y": ((rows, d), dt), "sum": None if residual is None else ((rows, d), dt), "rstd": ((rows,), torch.float32),
+            "codes": None if fmt == FMT_NATIVE else ((rows, d), torch.uint8),
+            "scale": {FMT_NATIVE: None, FMT_E4M3: ((rows,), torch.float32),
+                      FMT_MXFP8: ((rows, -(-d // 32)), torch.uint8)}[fmt]}
+    o = {}
+    for k, spec in want.items():
+        given = None if out is None else out.get(k)
+        if spec is None:
+            o[k] = None
+        elif given is not None:
+            _exactly(given, f"out[{k!r}]", spec[0], spec[1], dev)
+            o[k] = given
+    _on_cuda(dev)
+    for k, spec in want.items():
+        if k not in o:
+            o[k] = torch.empty(spec[0], dtype=spec[1], device=dev)
+    with _device_of(dev):
+        _check(_lib().moe_rmsnorm(MOE_BF16 if dt == torch.bfloat16 else MOE_F32, rows, d, _ptr(x), _ptr(residual),
+                                  _ptr(weight), eps, _ptr(o["sum"]), _ptr(o["y"]), fmt, _ptr(o["codes"]),
+                                  _ptr(o["scale"]), _ptr(o["rstd"]), _stream_of(dev, stream)), "moe_rmsnorm")
+    return o
+
+
+def rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                     dsum: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                     dweight: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None):
+    """moe_rmsnorm_backward: (dx, dweight) from the gradient dy of y; s is the forward's "sum" (x without a residual)
+    and rstd its "rstd".  dsum is the gradient that reaches the sum by other ways (the residual stream).  dx is the
+    gradient of x and of residual alike; dweight is fp32."""
+    _rows(s, "s")
+    rows, d = s.shape
+    dev, dt = s.device, s.dtype
+    _rows(dy, "dy", dt, s.shape, dev)
+    _exactly(weight, "weight", (d,), dt, dev)
+    _exactly(rstd, "rstd", (rows,), torch.float32, dev)
+    for name, t in (("dsum", dsum), ("dx", dx)):
+        if t is not None:
+            _rows(t, name, dt, s.shape, dev)
+    if dweight is not None:
+        _exactly(dweight, "dweight", (d,), torch.float32, dev)
+    _need(ws, "ws", 0, torch.uint8, dev)
+    _on_cuda(dev)
+    dtype = MOE_BF16 if dt == torch.bfloat16 else MOE_F32
+    n = int(_lib().moe_rmsnorm_backward_workspace_bytes(dtype, rows, d))
+    ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev) if ws is None else ws
+    dx = torch.empty_like(s) if dx is None else dx
+    dweight = torch.empty(d, dtype=torch.float32, device=dev) if dweight is None else dweight
+    with _device_of(dev):
+        _check(_lib().moe_rmsnorm_backward(dtype, rows, d, _ptr(dy), _ptr(s), _ptr(weight), _ptr(rstd), _ptr(dsum),
+                                           _ptr(dx), _ptr(dweight), _ptr(ws), ws.numel(), _stream_of(dev, stream)),
+               "moe_rmsnorm_backward")
+    return dx, dweight
+
+
+def grad_tensors(grads: Dict) -> list:
+    """The parameters' gradients of a layer_backward result (everything but dx), as a list for grad_norm / clip_grads."""
+    g = [grads["dcentroids"], grads.get("drouter_bias")]
+    for stack in (grads["routed"], grads["shared"]):
+        g += [] if stack is None else [stack.get(k) for k in ("w1", "b1", "w3", "b3", "w2", "b2")]
+    return [t for t in g if t is not None]
+
+
+def new_grad_workspace(device="cuda") -> torch.Tensor:
+    """Workspace of grad_norm and clip_grads (one for any list of tensors)."""
+    ws = torch.empty(int(_lib().moe_grad_workspace_bytes()), dtype=torch.uint8, device=device)
+    with _device_of(ws.device):
+        _check(_lib().moe_ws_init(_ptr(ws), ws.numel(), _stream_of(ws.device)), "moe_ws_init")
+    return ws
+
+
+def _tensor_list(tensors, name: str, device: torch.device):
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}[{i}] must be a torch.Tensor")
+        if t.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError(f"{name}[{i}] has dtype {t.dtype}; bfloat16 or float32 is needed")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+        if t.device != device:
+            raise ValueError(f"{name}[{i}] is on {t.device}; the workspace is on {device}")
+    return (MoeTensor * max(len(tensors), 1))(
+        *(MoeTensor(t.data_ptr(), t.numel(), MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32) for t in tensors))
+
+
+def _spans(tensors):
+    return [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i) for i, t in enumerate(tensors) if t.numel()]
+
+
+def _no_overlap(spans, what: str):
+    spans = sorted(spans)
+    for a, b in zip(spans, spans[1:]):
+        if b[0] < a[1]:
+            raise ValueError(f"{what} {a[2]} and {b[2]} overlap in memory")
+
+
+def _norm_out(norm, ws):
+    if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8:
+        raise TypeError("ws must be a workspace of new_grad_workspace")
+    _need(norm, "norm", 1, torch.float32, ws.device)
+    _on_cuda(ws.device)
+    return torch.empty((), dtype=torch.float32, device=ws.device) if norm is None else norm
+
+
+def grad_norm(tensors, ws: torch.Tensor, norm: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_grad_norm: the L2 norm over all elements of a list of bf16 and fp32 tensors, an fp32 scalar on the device (no
+    synchronisation).  ws from new_grad_workspace."""
+    tensors = list(tensors)
+    norm = _norm_out(norm, ws)
+    arr = _tensor_list(tensors, "tensors", ws.device)
+    with _device_of(ws.device):
+        _check(_lib().moe_grad_norm(arr, len(tensors), _ptr(norm), _ptr(ws), ws.numel(), _stream_of(ws.device, stream)),
+               "moe_grad_norm")
+    return norm
+
+
+def clip_grads(tensors, max_norm: float, ws: torch.Tensor, out=None, norm: Optional[torch.Tensor] = None,
+               stream=None) -> torch.Tensor:
+    """moe_clip_grads: scales the tensors by min(1, max_norm / (norm + 1e-6)), in place or into the tensors of `out` (same
+    sizes and types), and returns the norm before clipping, an fp32 scalar on the device (no synchronisation)."""
+    tensors = list(tensors)
+    norm = _norm_out(norm, ws)
+    arr = _tensor_list(tensors, "tensors", ws.device)
+    _no_overlap(_spans(tensors), "tensors")
+    oarr = None
+    if out is not None:
+        out = list(out)
+        oarr = _tensor_list(out, "out", ws.device)
+        if len(out) != len(tensors) or any(o.shape != t.shape or o.dtype != t.dtype for o, t in zip(out, tensors)):
+            raise ValueError("out must hold a tensor of the same shape and type for each gradient")
+        mine = {i: s[:2] for *s, i in _spans(tensors)}
+        _no_overlap([s for s in _spans(out) if mine[s[2]] != s[:2]] + _spans(tensors), "gradients and out")
+        _no_overlap(_spans(out), "out")
+    with _device_of(ws.device):
+        _check(_lib().moe_clip_grads(arr, oarr, len(tensors), float(max_norm), _ptr(norm), _ptr(ws), ws.numel(),
+                                     _stream_of(ws.device, stream)), "moe_clip_grads")
+    return norm
 
 
 def stage_events(stream=None, n_stages: int = NUM_STAGES):

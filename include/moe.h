@@ -472,6 +472,72 @@ moe_status_t moe_permute_no_alloc(const moe_shape_t* shape, const int32_t* topk_
                                   int32_t* counts, int32_t* offsets, int32_t* sorted_token,
                                   float* sorted_gate, int32_t* slot_of, moe_stream_t stream);
 
+/*
+ * Around the layer: what a transformer block runs directly before it, and what a training step runs
+ * on its gradients.  The pages leave both to the caller; the formulas are the usual definitions.
+ *
+ * RMS norm of the residual stream, with the residual's addition, and the rows in 8 bits beside the
+ * 16-bit ones for a layer with FP8 routed experts (moe_layer_forward_quantized).  Per row of d:
+ *   s    = x + residual, rounded to dtype (s = x without a residual)
+ *   rstd = 1 / sqrt(mean(s^2) + eps)                 (fp32, from the rounded s)
+ *   v    = s * rstd * weight                         (fp32, not rounded before what follows)
+ *   y    = v rounded to dtype
+ *   fmt MOE_FMT_E4M3:  scales [rows] fp32 = max|v| / 448 (1 for an all-zero row, at least 2^-126),
+ *                      codes [rows, d] = e4m3 of v / scale, round to nearest even, saturating
+ *   fmt MOE_FMT_MXFP8: scales [rows, ceil(d / 32)] bytes e + 127, e as for the weights' runs of 32;
+ *                      codes [rows, d] = e4m3 of v * 2^-e
+ * The codes are rounded once, from v: they can differ in the last step from what
+ * moe_quantize_rows_e4m3 makes of the rounded y.
+ *   x, residual, sum, y: [rows, d] dtype; weight: [d] dtype; residual and sum both NULL or both given;
+ *   sum may be residual or x itself (in place).  codes and scales NULL iff fmt is MOE_FMT_NATIVE; the
+ *   8-bit formats need MOE_BF16.  rstd: [rows] fp32 out, or NULL.
+ * Sizes: 0 <= rows < 2^31, 1 <= d <= 16384; MOE_BF16: d a multiple of 8 and 16-byte aligned pointers.
+ * codes 16-byte aligned.  Needs no workspace; nothing can fail on the device.
+ */
+moe_status_t moe_rmsnorm(int32_t dtype, int64_t rows, int32_t d, const void* x, const void* residual,
+                         const void* weight, float eps, void* sum, void* y, int32_t fmt, uint8_t* codes, void* scales,
+                         float* rstd, moe_stream_t stream);
+
+/*
+ * Gradients of moe_rmsnorm: with xhat = s * rstd and g = dy * weight,
+ *   dx      = rstd * (g - xhat * mean(g * xhat)) + dsum    (the gradient of x and of residual alike)
+ *   dweight = sum over the rows of dy * xhat
+ *   dy, s (the forward's sum, or x), dsum (the gradient that reaches sum by other ways; NULL: none) and
+ *   dx: [rows, d] dtype; rstd [rows] as the forward wrote it; dweight [d] fp32.  The eight-bit outputs
+ *   carry no gradient of their own.  dx may be dy or dsum itself.  Fixed summation order.
+ * ws: moe_rmsnorm_backward_workspace_bytes(dtype, rows, d) bytes (0 for sizes outside the rules above),
+ * scratch only.  rows == 0 writes a zero dweight.
+ */
+size_t moe_rmsnorm_backward_workspace_bytes(int32_t dtype, int64_t rows, int32_t d);
+moe_status_t moe_rmsnorm_backward(int32_t dtype, int64_t rows, int32_t d, const void* dy, const void* s,
+                                  const void* weight, const float* rstd, const void* dsum, void* dx, float* dweight,
+                                  void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* One tensor of a list: `numel` consecutive elements of dtype at `data` (any alignment its type allows). */
+typedef struct {
+    void* data;
+    int64_t numel; /* 0 allowed (data may then be NULL), < 2^40 */
+    int32_t dtype; /* moe_dtype_t */
+} moe_tensor_t;
+
+/*
+ * The global L2 norm of the gradients of a step, and clipping by it (the gradients of
+ * moe_layer_backward and moe_rmsnorm_backward, of any number of layers):
+ *   norm = sqrt(sum over all elements of g^2)      (fp32 [1] out, DEVICE memory; no host synchronisation)
+ *   moe_clip_grads: coef = min(1, max_norm / (norm + 1e-6)), out = g * coef rounded to dtype
+ * grads, out: HOST arrays of n descriptors (n <= 65536), read before the call returns; out NULL clips
+ * in place (and writes nothing when coef is 1), else tensors of the same sizes and types that do not
+ * overlap the gradients of other entries.  Squares below fp32's range or above it are taken in 64 bits.
+ * A norm of infinity gives coef 0 (infinite elements become NaN), a NaN norm gives NaN gradients.
+ * max_norm must not be negative or NaN (infinity: no clipping).  No tensor may be listed twice.
+ * ws: moe_grad_workspace_bytes() bytes, cleared once by moe_ws_init; sums in fixed order.
+ */
+size_t moe_grad_workspace_bytes(void);
+moe_status_t moe_grad_norm(const moe_tensor_t* grads, int32_t n, float* norm, void* ws, size_t ws_bytes,
+                           moe_stream_t stream);
+moe_status_t moe_clip_grads(const moe_tensor_t* grads, const moe_tensor_t* out, int32_t n, float max_norm, float* norm,
+                            void* ws, size_t ws_bytes, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,104 @@
+"""Refusals of the operators around the layer (CPU): the binding's checks and the C entry points' own, before any
+CUDA call."""
+import ctypes
+import math
+
+import pytest
+import torch
+
+from fine_grained_mixture_route_b200 import moe
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _m(rows, d, dtype=BF):
+    return torch.zeros((rows, d), dtype=dtype)
+
+
+def test_rmsnorm_refuses_before_any_call():
+    x, w = _m(4, 64), torch.ones(64, dtype=BF)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.rmsnorm(x, w)
+    for bad, what in ((dict(x=x.half()), "dtype"), (dict(x=x[:, ::2]), "contiguous"), (dict(x=x[0]), "matrix"),
+                      (dict(weight=w.float()), "weight has dtype"), (dict(weight=torch.ones(63, dtype=BF)), "weight has shape"),
+                      (dict(residual=_m(5, 64)), "residual has shape"), (dict(residual=_m(4, 64, F32)), "residual has dtype"),
+                      (dict(fmt=7), "fmt"), (dict(out={"y": _m(4, 63)}), "out"), (dict(out={"rstd": torch.zeros(5)}), "out"),
+                      (dict(fmt=moe.FMT_MXFP8, out={"scale": torch.zeros((4, 3), dtype=torch.uint8)}), "out")):
+        args = dict(x=x, weight=w)
+        args.update(bad)
+        with pytest.raises((ValueError, TypeError), match=what):
+            moe.rmsnorm(**args)
+    with pytest.raises(TypeError):
+        moe.rmsnorm([1.0], w)
+
+
+def test_rmsnorm_backward_refuses_before_any_call():
+    s, w, r = _m(4, 64), torch.ones(64, dtype=BF), torch.ones(4)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.rmsnorm_backward(s, s, w, r)
+    for bad, what in ((dict(dy=_m(4, 63)), "dy has shape"), (dict(dy=_m(4, 64, F32)), "dy has dtype"),
+                      (dict(rstd=torch.ones(5)), "rstd has shape"), (dict(rstd=torch.ones(4, dtype=BF)), "rstd has dtype"),
+                      (dict(dsum=_m(3, 64)), "dsum has shape"), (dict(dx=_m(4, 64, F32)), "dx has dtype"),
+                      (dict(dweight=torch.zeros(63)), "dweight has shape"), (dict(ws=torch.zeros(4)), "ws has dtype")):
+        args = dict(dy=s, s=s, weight=w, rstd=r)
+        args.update(bad)
+        with pytest.raises((ValueError, TypeError), match=what):
+            moe.rmsnorm_backward(**args)
+
+
+def test_grad_lists_refused():
+    ws = torch.zeros(1 << 14, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.grad_norm([torch.zeros(4)], ws)
+    with pytest.raises(TypeError):
+        moe.grad_norm([torch.zeros(4)], torch.zeros(4))
+    for bad, what in (([torch.zeros(4).half()], "dtype"), ([torch.zeros((4, 4))[:, :2]], "contiguous"), ([3.0], "Tensor")):
+        with pytest.raises((ValueError, TypeError), match=what):
+            moe._tensor_list(bad, "tensors", torch.device("cpu"))
+    t = torch.zeros(100)
+    with pytest.raises(ValueError, match="overlap"):
+        moe._no_overlap(moe._spans([t[:50], t[49:]]), "tensors")
+    with pytest.raises(ValueError, match="overlap"):
+        moe._no_overlap(moe._spans([t, t]), "tensors")          # the same gradient twice
+    moe._no_overlap(moe._spans([t[:50], t[50:], t[:0]]), "tensors")
+
+
+def test_c_entry_points_return_errors():
+    lib, INV, UNS, WS = moe.lib_handle(), moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED, moe.MOE_ERR_WORKSPACE
+    p, odd = ctypes.c_void_p(1 << 40), ctypes.c_void_p((1 << 40) + 8)      # never dereferenced
+
+    def norm(dtype=1, rows=4, d=64, x=p, res=None, w=p, eps=1e-6, s=None, y=p, fmt=0, codes=None, sc=None, rstd=None):
+        return lib.moe_rmsnorm(dtype, rows, d, x, res, w, eps, s, y, fmt, codes, sc, rstd, None)
+
+    assert norm(rows=0, x=None, y=None) == moe.MOE_OK
+    for kw in (dict(dtype=2), dict(rows=-1), dict(d=0), dict(x=None), dict(w=None), dict(y=None), dict(res=p), dict(s=p),
+               dict(fmt=3), dict(codes=p), dict(fmt=1, codes=p), dict(fmt=2, sc=p), dict(eps=-1.0), dict(eps=math.nan),
+               dict(eps=math.inf), dict(x=odd), dict(y=odd), dict(w=odd), dict(fmt=1, codes=odd, sc=p)):
+        assert norm(**kw) == INV, kw
+    for kw in (dict(d=60), dict(d=16392), dict(rows=1 << 31), dict(dtype=0, fmt=1, codes=p, sc=p), dict(dtype=0, d=16385)):
+        assert norm(**kw) == UNS, kw
+    need = lib.moe_rmsnorm_backward_workspace_bytes
+    assert need(1, 4, 64) >= 256 and need(1, 100000, 7168) >= 7168 * 4 and need(1, 4, 60) == 0 and need(5, 4, 64) == 0
+
+    def bwd(dtype=1, rows=4, d=64, dy=p, s=p, w=p, r=p, ds=None, dx=p, dw=p, ws=p, n=1 << 30):
+        return lib.moe_rmsnorm_backward(dtype, rows, d, dy, s, w, r, ds, dx, dw, ws, n, None)
+
+    for kw in (dict(dy=None), dict(s=None), dict(w=None), dict(r=None), dict(dx=None), dict(dw=None), dict(ds=odd), dict(dx=odd)):
+        assert bwd(**kw) == INV, kw
+    for kw in (dict(ws=None), dict(n=16), dict(ws=odd)):
+        assert bwd(**kw) == WS, kw
+    assert bwd(d=60) == UNS
+
+    T = lambda **k: (moe.MoeTensor * 1)(moe.MoeTensor(*[{**dict(data=1 << 40, numel=8, dtype=1), **k}[f]  # noqa: E731
+                                                         for f in ("data", "numel", "dtype")]))
+    n = lib.moe_grad_workspace_bytes()
+    for t in (T(dtype=3), T(numel=-1), T(data=0), T(data=(1 << 40) + 1), T(data=(1 << 40) + 2, dtype=0)):
+        assert lib.moe_grad_norm(t, 1, p, p, n, None) == INV
+    assert lib.moe_grad_norm(T(numel=1 << 40), 1, p, p, n, None) == UNS
+    assert lib.moe_grad_norm(T(), 70000, p, p, n, None) == UNS
+    assert lib.moe_grad_norm(T(), 1, None, p, n, None) == INV and lib.moe_grad_norm(None, 1, p, p, n, None) == INV
+    assert lib.moe_grad_norm(T(), 1, p, p, n - 1, None) == WS and lib.moe_grad_norm(T(), 1, p, None, n, None) == WS
+    for m in (-1.0, math.nan):
+        assert lib.moe_clip_grads(T(), None, 1, m, p, p, n, None) == INV
+    assert lib.moe_clip_grads(T(), T(numel=9), 1, 1.0, p, p, n, None) == INV
+    assert lib.moe_clip_grads(T(), T(dtype=0), 1, 1.0, p, p, n, None) == INV

@@ -1,0 +1,207 @@
+"""RMS norm (moe.rmsnorm, moe.rmsnorm_backward) against 64-bit plain forms (B200)."""
+import pytest
+import torch
+
+from fine_grained_mixture_route_b200 import moe
+from tests import block_ref as R
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+def _inputs(rows, d, dtype, seed=0, residual=True):
+    g = torch.Generator(device="cuda").manual_seed(seed + 7919 * d + rows)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x = n(rows, d).to(dtype)
+    res = (n(rows, d) * n(rows, 1).exp()).to(dtype) if residual else None
+    if residual:
+        res[:, ::5] *= 16                                       # channels far larger than the others
+    return x, res, (1 + 0.2 * n(d)).to(dtype)
+
+
+def _check_rows(o, x, res, w, eps, fmt):
+    s, r, v = R.forward(x, res, w, eps)
+    dt = x.dtype
+    if res is not None:
+        assert torch.equal(o["sum"], (x.float() + res.float()).to(dt))
+        s = o["sum"].double()
+        r = R.rms(s, eps)
+        v = s * r[:, None] * w.double()
+    else:
+        assert o["sum"] is None
+    assert ((o["rstd"].double() - r).abs() <= R.F32 * r).all()
+    y = o["y"].double()
+    half = R.HALF[dt]
+    assert ((y - v).abs() <= (half + R.F32) * v.abs() + 1e-38).all()
+    if fmt == moe.FMT_NATIVE:
+        assert o["codes"] is None and o["scale"] is None
+        return
+    q = o["codes"].view(torch.float8_e4m3fn).double()
+    if fmt == moe.FMT_E4M3:
+        amax = v.abs().amax(1)
+        sc = torch.where(amax > 0, amax / 448.0, torch.ones_like(amax))
+        assert ((o["scale"].double() - sc).abs() <= 2 * R.F32 * sc).all()
+        u = v / o["scale"].double()[:, None]
+    else:
+        rows, d = v.shape
+        nr = -(-d // 32)
+        p = torch.zeros((rows, nr * 32), dtype=torch.float64, device=v.device)
+        p[:, :d] = v
+        amax = p.view(rows, nr, 32).abs().amax(2)
+        e = o["scale"].double() - 127.0
+        lo, hi = R.run_exponents(amax * (1 - 2 * R.F32)), R.run_exponents(amax * (1 + 2 * R.F32))
+        assert (((e == lo) | (e == hi))).all()                  # the two differ only next to a border
+        u = v / torch.pow(2.0, e).repeat_interleave(32, 1)[:, :d]
+    # normal codes: half a step relative; below 2^-6: half of the step 2^-9; above 448 by v's own error only
+    assert ((q - u).abs() <= (2.0 ** -4 + 4 * R.F32) * u.abs() + 2.0 ** -10).all()
+    assert (q.abs() <= 448).all()
+
+
+@pytest.mark.parametrize("rows,d", [(1, 8), (1, 7168), (3, 264), (37, 1024), (700, 1032), (301, 2056), (600, 8),
+                                    (1200, 248), (5, 16384), (400, 16384), (333, 7168)])
+@pytest.mark.parametrize("fmt", [moe.FMT_NATIVE, moe.FMT_E4M3, moe.FMT_MXFP8])
+@pytest.mark.parametrize("residual", [True, False])
+def test_rows_bf16(rows, d, fmt, residual):
+    x, res, w = _inputs(rows, d, torch.bfloat16, residual=residual)
+    _check_rows(moe.rmsnorm(x, w, eps=EPS, residual=res, fmt=fmt), x, res, w, EPS, fmt)
+
+
+@pytest.mark.parametrize("rows,d", [(1, 1), (7, 3), (500, 33), (2, 1023), (2, 16383), (700, 16383), (3, 4096), (900, 256),
+                                    (350, 4100)])
+def test_rows_fp32_of_any_width(rows, d):
+    x, res, w = _inputs(rows, d, torch.float32)
+    _check_rows(moe.rmsnorm(x, w, eps=EPS, residual=res), x, res, w, EPS, moe.FMT_NATIVE)
+
+
+def test_fp32_rows_off_16_byte_alignment():
+    base = torch.randn(9 * 64 + 1, device="cuda")
+    x = base[1:].view(9, 64)
+    w = torch.ones(64, device="cuda")
+    _check_rows(moe.rmsnorm(x, w), x, None, w, 1e-6, moe.FMT_NATIVE)
+
+
+def test_special_rows():
+    d = 256
+    x = torch.randn(6, d, device="cuda").bfloat16()
+    x[0] = 0                                                   # a padded row
+    x[1] = 1e-30                                               # squares below fp32's range
+    x[2, 5] = float("inf")
+    x[3, 7] = float("nan")
+    x[4, :32] = 0                                              # a run of zeros
+    w = torch.ones(d, device="cuda", dtype=torch.bfloat16)
+    for fmt in (moe.FMT_NATIVE, moe.FMT_E4M3, moe.FMT_MXFP8):
+        o = moe.rmsnorm(x, w, fmt=fmt)
+        assert (o["y"][0] == 0).all() and torch.isfinite(o["y"][[0, 1, 4, 5]]).all()
+        assert torch.isnan(o["y"][2, 5]) and (o["y"][2, :5] == 0).all()     # inf * 0, and the others over infinity
+        assert torch.isnan(o["y"][3]).all()
+        keep = [0, 1, 4, 5]
+        part = {k: (None if v is None else v[keep]) for k, v in o.items()}
+        _check_rows(part, x[keep], None, w, 1e-6, fmt)
+        if fmt == moe.FMT_E4M3:
+            assert o["scale"][0] == 1 and (o["codes"][0] == 0).all()
+        if fmt == moe.FMT_MXFP8:
+            assert (o["scale"][0] == 127).all() and o["scale"][4, 0] == 127
+
+
+def test_rows_are_independent_and_in_place_sum():
+    x, res, w = _inputs(400, 1536, torch.bfloat16)
+    one = moe.rmsnorm(x, w, residual=res, fmt=moe.FMT_MXFP8)
+    part = moe.rmsnorm(x[17:18].contiguous(), w, residual=res[17:18].contiguous(), fmt=moe.FMT_MXFP8)
+    s = res.clone()
+    inp = moe.rmsnorm(x, w, residual=s, fmt=moe.FMT_MXFP8, out={"sum": s})
+    assert inp["sum"] is s
+    for k in ("y", "sum", "codes", "scale", "rstd"):
+        assert torch.equal(one[k], inp[k]), k
+        # one row alone takes another split of the row over the threads: equal up to the sum's order
+        assert ((one[k][17:18].double() - part[k].double()).abs() <= 2 * one[k][17:18].double().abs()).all()
+    assert ((one["rstd"][17:18] - part["rstd"]).abs() <= 2 * R.F32 * part["rstd"]).all()
+
+
+def test_offsets_past_31_bits():
+    rows, d = 300_001, 7168                                    # 2.15e9 elements
+    x = torch.zeros((rows, d), dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(3, d, device="cuda").bfloat16()
+    x[-3:] = tail
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    o = moe.rmsnorm(x, w, fmt=moe.FMT_E4M3)
+    last = {k: (None if v is None else v[-3:]) for k, v in o.items()}
+    _check_rows(last, tail, None, w, 1e-6, moe.FMT_E4M3)
+    assert (o["y"][-4] == 0).all() and o["scale"][-4] == 1
+
+
+@pytest.mark.parametrize("rows,d,dtype", [(1, 8, torch.bfloat16), (5, 7168, torch.bfloat16), (1000, 2048, torch.bfloat16),
+                                          (2500, 264, torch.bfloat16), (900, 7168, torch.bfloat16),
+                                          (310, 16384, torch.bfloat16), (64, 1, torch.float32), (333, 35, torch.float32),
+                                          (20, 16383, torch.float32), (600, 1028, torch.float32), (310, 8200, torch.float32),
+                                          (2600, 64, torch.float32)])
+@pytest.mark.parametrize("dsum", [True, False])
+def test_backward(rows, d, dtype, dsum):
+    s, ds, w = _inputs(rows, d, dtype, seed=1)
+    dy = _inputs(rows, d, dtype, seed=2, residual=False)[0]
+    ds = ds if dsum else None
+    rstd = R.rms(s.double(), EPS).float()
+    dx, dw = moe.rmsnorm_backward(dy, s, w, rstd, dsum=ds)
+    ref, size, rw, rw_size = R.backward(dy, s, w, rstd, ds)
+    assert ((dx.double() - ref).abs() <= R.HALF[dtype] * ref.abs() + 2 * R.F32 * size).all()
+    # a column's sum: at most ceil(rows / blocks) additions in a thread, then 32 warps' partials and their tree
+    n = rows + 64
+    assert ((dw.double() - rw).abs() <= n * 2.0 ** -24 * rw_size + 1e-30).all()
+    again = moe.rmsnorm_backward(dy, s, w, rstd, dsum=ds)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+def test_backward_against_differences():
+    rows, d = 3, 40
+    s, _, w = _inputs(rows, d, torch.float32, seed=3, residual=False)
+    dy = torch.randn(rows, d, device="cuda")
+    o = moe.rmsnorm(s, w, eps=EPS)
+    dx, dw = moe.rmsnorm_backward(dy, s, w, o["rstd"])
+    f = lambda a, b: float((R.forward(a, None, b, EPS)[2] * dy.double()).sum())  # noqa: E731
+    h = 1e-5
+    for i, j in ((0, 0), (1, 17), (2, 39)):
+        up, dn = s.double().clone(), s.double().clone()
+        up[i, j] += h
+        dn[i, j] -= h
+        assert abs((f(up, w.double()) - f(dn, w.double())) / (2 * h) - float(dx[i, j])) <= 1e-4
+    for j in (0, 39):
+        up, dn = w.double().clone(), w.double().clone()
+        up[j] += h
+        dn[j] -= h
+        assert abs((f(s.double(), up) - f(s.double(), dn)) / (2 * h) - float(dw[j])) <= 1e-4
+
+
+def test_backward_in_place_and_empty():
+    s, ds, w = _inputs(200, 512, torch.bfloat16)
+    dy = torch.randn(200, 512, device="cuda").bfloat16()
+    rstd = moe.rmsnorm(s, w)["rstd"]
+    want = moe.rmsnorm_backward(dy, s, w, rstd, dsum=ds)
+    buf = ds.clone()
+    got = moe.rmsnorm_backward(dy, s, w, rstd, dsum=buf, dx=buf)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    e = torch.empty((0, 512), dtype=torch.bfloat16, device="cuda")
+    dx, dw = moe.rmsnorm_backward(e, e, w, torch.empty(0, device="cuda"))
+    assert dx.shape == (0, 512) and (dw == 0).all()
+    o = moe.rmsnorm(e, w, fmt=moe.FMT_MXFP8)
+    assert o["y"].shape == (0, 512) and o["scale"].shape == (0, 16)
+
+
+def test_captured_on_a_side_stream():
+    x, res, w = _inputs(64, 1024, torch.bfloat16)
+    want = moe.rmsnorm(x, w, residual=res, fmt=moe.FMT_E4M3)
+    dwant = moe.rmsnorm_backward(x, want["sum"], w, want["rstd"], dsum=res)
+    out = {k: (None if v is None else torch.empty_like(v)) for k, v in want.items()}
+    dx, dw = torch.empty_like(x), torch.empty_like(dwant[1])
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        moe.rmsnorm(x, w, residual=res, fmt=moe.FMT_E4M3, out=out)
+        moe.rmsnorm_backward(x, out["sum"], w, out["rstd"], dsum=res, dx=dx, dweight=dw, ws=ws)
+    for _ in range(2):
+        for t in (*[v for v in out.values() if v is not None], dx, dw):
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out[k], want[k]) for k in want)
+        assert torch.equal(dx, dwant[0]) and torch.equal(dw, dwant[1])
