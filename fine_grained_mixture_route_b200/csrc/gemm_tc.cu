@@ -44,6 +44,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "pipe.cuh"
 
 namespace moe {
 namespace tc {
@@ -74,7 +75,6 @@ constexpr int SFA_BYTES = 512;                                   // A scales of 
 constexpr uint32_t SFA_COL = 2 * ACC_COLS - MX_OVL;            // 480
 constexpr uint32_t SFB_COL = SFA_COL + 8;                        // 488
 constexpr int SMEM_BYTES_Q8 = SMEM_BYTES + 4 * (SF_STAGE_BYTES + SFA_BYTES);
-constexpr unsigned long long WAIT_NS = 4000000000ull;
 #ifndef MOE_GROUP_M
 #define MOE_GROUP_M 8                    // M-tiles per raster band of the expert GEMMs
 #endif
@@ -166,61 +166,6 @@ struct Params {
 };
 
 // ------------------------------------------------------------------------------ PTX helpers
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-__device__ __forceinline__ unsigned long long globaltimer() {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// Bounded wait on the phase `parity` of an mbarrier: true once it completes; false when the
-// pipeline was aborted (abort_flag set by another role) or the wait gave up after limit_ns of
-// %globaltimer or WAIT_MAX_POLLS polls, whichever comes first; giving up sets abort_flag and
-// error bit 2.
-constexpr uint32_t WAIT_MAX_POLLS = 1u << 30;
-__device__ __forceinline__ bool mbar_wait_limit(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
-                                                bool honour_abort, unsigned long long limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer();
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63u) == 0u) {
-            if (honour_abort && *abort_flag) return false;
-            if (globaltimer() - t0 > limit_ns || i >= WAIT_MAX_POLLS) {
-                *abort_flag = 1;
-                flag_error(err, ERR_PIPE_TIMEOUT);
-                return false;
-            }
-        }
-    }
-}
-// The pipeline's wait: a few seconds at most.
-__device__ __noinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
-                                       bool honour_abort = true) {
-    return mbar_wait_limit(bar, parity, abort_flag, err, honour_abort, WAIT_NS);
-}
-
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
@@ -349,14 +294,6 @@ __device__ __forceinline__ uint64_t sf_desc(uint32_t addr) {
 __device__ __forceinline__ void tmem_cp_sf(uint32_t taddr, uint64_t sdesc) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
-// Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) global -> shared,
-// completing on the mbarrier's transaction count.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }

@@ -282,6 +282,15 @@ constexpr int GRAD_BLOCKS = 1024;             // partial sums in the workspace
 constexpr int GRAD_STATE_OFFSET = 16;         // in the workspace's first 256 bytes
 constexpr int GRAD_MAX_TENSORS = 65536, GRAD_MAX_LAUNCHES = 512;
 size_t grad_workspace_bytes();
+// The whole layer for up to MOE_FEW_MAX_TOKENS tokens in one kernel (few.cu); ws of few_workspace_bytes, its
+// first 256 bytes cleared once.
+constexpr int FEW_MAX_D = 32768;
+constexpr int FEW_BARRIER_OFFSET = 64;        // in the workspace's first 256 bytes
+bool few_supported(const Dims& D);
+size_t few_workspace_bytes(const Dims& D);
+cudaError_t launch_few(const Dims& D, const void* x, const void* cen, const float* rbias, const FfnWeights& R,
+                       const FfnWeights& Sh, void* out, int32_t* idx, float* gate, int32_t* counts, void* ws,
+                       cudaStream_t stream);
 cudaError_t launch_grad_norm(const moe_tensor_t* t, const moe_tensor_t* out, int n, float max_norm, float* norm, void* ws,
                              cudaStream_t stream);
 

@@ -351,7 +351,8 @@ MOE_EXPORT moe_status_t moe_check_device_error(void* ws, size_t ws_bytes, moe_st
     if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
     if (detail) *detail = h;
     if (h) {
-        if (cudaMemsetAsync(ws, 0, sizeof(h), st) != cudaSuccess) return MOE_ERR_CUDA;
+        // the whole header: a few-token kernel that gave up leaves its grid barriers between two rounds
+        if (cudaMemsetAsync(ws, 0, 256, st) != cudaSuccess) return MOE_ERR_CUDA;
         if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
         return MOE_ERR_INTERNAL;
     }
@@ -719,6 +720,37 @@ MOE_EXPORT moe_status_t moe_layer_forward_timed(const moe_shape_t* shape, const 
     return layer_forward_impl(shape, x, centroids, router_bias, routed, shared, out, topk_idx_out, topk_gate_out,
                               counts_out, ws, ws_bytes, (cudaStream_t)stream,
                               reinterpret_cast<cudaEvent_t const*>(stage_events));
+}
+
+MOE_EXPORT size_t moe_few_workspace_bytes(const moe_shape_t* shape) {
+    Dims D;
+    if (to_dims(shape, &D) != MOE_OK || !few_supported(D)) return 0;
+    return few_workspace_bytes(D);
+}
+
+MOE_EXPORT moe_status_t moe_layer_forward_few(const moe_shape_t* shape, const void* x, const void* centroids,
+                                              const float* router_bias, const moe_ffn_weights_t* routed,
+                                              const moe_ffn_weights_t* shared, void* out, int32_t* topk_idx_out,
+                                              float* topk_gate_out, int32_t* counts_out, void* ws, size_t ws_bytes,
+                                              moe_stream_t stream) {
+    Dims D;
+    MOE_TRY(to_dims(shape, &D));
+    if (!few_supported(D)) return MOE_ERR_UNSUPPORTED;
+    if (!centroids || (D.T > 0 && (!x || !out))) return MOE_ERR_INVALID_ARG;
+    MOE_TRY(check_weights(D, routed, true));
+    if (D.Ks > 0) MOE_TRY(check_weights(D, shared));
+    else if (shared) return MOE_ERR_INVALID_ARG;
+    uintptr_t a = (uintptr_t)x | (uintptr_t)centroids | (uintptr_t)out | (uintptr_t)routed->w1 | (uintptr_t)routed->w3 |
+                  (uintptr_t)routed->w2;
+    if (shared) a |= (uintptr_t)shared->w1 | (uintptr_t)shared->w3 | (uintptr_t)shared->w2;
+    if (a & 15u) return MOE_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < few_workspace_bytes(D) || ((uintptr_t)ws & 15u)) return MOE_ERR_WORKSPACE;
+    if (D.T == 0) return MOE_OK;
+    MOE_TRY(check_device());
+    cudaGetLastError();
+    MOE_CUDA(launch_few(D, x, centroids, router_bias, to_ffn(routed), to_ffn(shared), out, topk_idx_out, topk_gate_out,
+                        counts_out, ws, (cudaStream_t)stream));
+    return MOE_OK;
 }
 
 MOE_EXPORT size_t moe_train_ctx_bytes(const moe_shape_t* shape) {

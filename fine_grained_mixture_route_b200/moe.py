@@ -28,7 +28,9 @@ EXPORTED = ("moe_workspace_bytes", "moe_layer_launches", "moe_status_string", "m
             "moe_layer_backward_timed", "moe_backward_launches", "moe_balance_workspace_bytes",
             "moe_balance_stats", "moe_gather_rows", "moe_segment_ids", "moe_selftest_wait_timeout",
             "moe_mx_scale_bytes", "moe_quantize_weights_mx", "moe_rmsnorm", "moe_rmsnorm_backward",
-            "moe_rmsnorm_backward_workspace_bytes", "moe_grad_workspace_bytes", "moe_grad_norm", "moe_clip_grads")
+            "moe_rmsnorm_backward_workspace_bytes", "moe_grad_workspace_bytes", "moe_grad_norm", "moe_clip_grads",
+            "moe_few_workspace_bytes", "moe_layer_forward_few")
+FEW_MAX_TOKENS = 16                          # MOE_FEW_MAX_TOKENS
 NUM_STAGES = 7
 STAGE_NAMES = ("router", "permute", "plan", "gather", "gemm1_swiglu", "gemm2", "combine")
 BWD_STAGES = 7
@@ -123,7 +125,10 @@ def _lib():
         lib.moe_grad_workspace_bytes.restype = sz
         lib.moe_grad_norm.argtypes = [tp, i32, f32p, vp, sz, vp]
         lib.moe_clip_grads.argtypes = [tp, tp, i32, f32, f32p, vp, sz, vp]
-        for n in ("moe_rmsnorm", "moe_rmsnorm_backward", "moe_grad_norm", "moe_clip_grads"):
+        lib.moe_few_workspace_bytes.argtypes = [sh]
+        lib.moe_few_workspace_bytes.restype = sz
+        lib.moe_layer_forward_few.argtypes = lib.moe_layer_forward.argtypes
+        for n in ("moe_rmsnorm", "moe_rmsnorm_backward", "moe_grad_norm", "moe_clip_grads", "moe_layer_forward_few"):
             getattr(lib, n).restype = ctypes.c_int
         for n in ("moe_check_device_error", "moe_ws_init", "moe_route", "moe_permute", "moe_expert_ffn",
                   "moe_combine", "moe_layer_forward", "moe_layer_forward_timed", "moe_quantize_rows_e4m3",
@@ -570,6 +575,40 @@ def selftest_wait_timeout(limit_ns: int, ws: torch.Tensor, out: Optional[torch.T
     _need(out, "out", 2, torch.int64, ws.device)
     _check(_lib().moe_selftest_wait_timeout(limit_ns, _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_selftest_wait_timeout")
+    return out
+
+
+# ----------------------------------------------------------------------------- a few tokens
+def few_workspace_bytes(shape: MoeShape) -> int:
+    """Bytes layer_forward_few needs (0: the shape is not supported there)."""
+    return int(_lib().moe_few_workspace_bytes(ctypes.byref(shape)))
+
+
+def new_few_workspace(shape: MoeShape, device="cuda") -> torch.Tensor:
+    """Workspace of layer_forward_few: for this shape and any that needs no more bytes (fewer tokens of the same layer)."""
+    n = few_workspace_bytes(shape)
+    if n == 0:
+        raise ValueError(f"layer shape not supported for a few tokens (at most {FEW_MAX_TOKENS})")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with _device_of(ws.device):
+        _check(_lib().moe_ws_init(_ptr(ws), n, _stream_of(ws.device)), "moe_ws_init")
+    return ws
+
+
+def layer_forward_few(shape: MoeShape, x, centroids, routed: Dict, shared: Optional[Dict], ws, out=None, idx=None,
+                      gate=None, counts=None, stream=None, router_bias=None):
+    """The whole layer for up to FEW_MAX_TOKENS tokens in one kernel (moe_layer_forward_few): layer_forward's arguments
+    and outputs, ws from new_few_workspace.  FP8 routed experts' activations are not quantised here."""
+    dev = _need_layer(shape, x, centroids, routed, shared, out, idx, gate, counts, router_bias)
+    _need(ws, "ws", 0, torch.uint8, dev)
+    _on_cuda(dev)
+    out = torch.empty((shape.T, shape.d), dtype=x.dtype, device=dev) if out is None else out
+    rw, sw = _weights(routed), _weights(shared)
+    with _device_of(dev):
+        _check(_lib().moe_layer_forward_few(ctypes.byref(shape), _ptr(x), _ptr(centroids), _bias_ptr(router_bias),
+                                            ctypes.byref(rw), None if sw is None else ctypes.byref(sw), _ptr(out),
+                                            _ptr(idx), _ptr(gate), _ptr(counts), _ptr(ws), ws.numel(),
+                                            _stream_of(dev, stream)), "moe_layer_forward_few")
     return out
 
 

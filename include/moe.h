@@ -538,6 +538,34 @@ moe_status_t moe_grad_norm(const moe_tensor_t* grads, int32_t n, float* norm, vo
 moe_status_t moe_clip_grads(const moe_tensor_t* grads, const moe_tensor_t* out, int32_t n, float max_norm, float* norm,
                             void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/*
+ * The whole layer for a few tokens (T <= MOE_FEW_MAX_TOKENS: the steps of a decoding batch, a drafted
+ * continuation) in one kernel: the same layer as moe_layer_forward, with the same arguments, gate modes,
+ * expert formats and optional outputs, bound by reading each picked expert's weights once.
+ * With FP8 routed experts (MOE_FMT_E4M3, MOE_FMT_MXFP8) the weights are the codes times their scales, as
+ * everywhere, but the activations are NOT quantised: with few tokens nothing is gained by it, and the
+ * result is the layer's on the dequantised weights.  So it can differ from moe_layer_forward's, which
+ * quantises them, by that quantisation.  Hidden values keep 16 significant bits (fp32 layers: 24); sums are
+ * fp32, in an order that depends on sizes and picks alone.
+ * A pick that does not exist (NaN logits, or all other keys -infinity) sets error bit 1 and is left out.
+ * Sizes: as the layer's, T <= MOE_FEW_MAX_TOKENS, d <= 32768, and for MOE_F32 d, inter and inter_shared
+ * multiples of 4 (MOE_ERR_UNSUPPORTED otherwise); x, centroids, out and all matrices 16-byte aligned
+ * (MOE_ERR_INVALID_ARG otherwise).
+ * ws: moe_few_workspace_bytes(shape) bytes (0 for a shape that is not supported), cleared once by
+ * moe_ws_init: the kernel's grid barriers count in it from call to call.  A workspace serves any supported
+ * shape that needs at most its size.  Calls that share one must not overlap.  The kernel is launched
+ * cooperatively, a block on every SM: it starts when the stream's turn comes and all SMs are free.
+ * Every wait is bounded; one that gives up sets error bit 2, and moe_check_device_error then clears the
+ * barriers too.  Can be captured into a graph.
+ */
+#define MOE_FEW_MAX_TOKENS 16
+size_t moe_few_workspace_bytes(const moe_shape_t* shape);
+moe_status_t moe_layer_forward_few(const moe_shape_t* shape, const void* x, const void* centroids,
+                                   const float* router_bias, const moe_ffn_weights_t* routed,
+                                   const moe_ffn_weights_t* shared, void* out, int32_t* topk_idx_out,
+                                   float* topk_gate_out, int32_t* counts_out, void* ws, size_t ws_bytes,
+                                   moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -102,3 +102,68 @@ def test_c_entry_points_return_errors():
         assert lib.moe_clip_grads(T(), None, 1, m, p, p, n, None) == INV
     assert lib.moe_clip_grads(T(), T(numel=9), 1, 1.0, p, p, n, None) == INV
     assert lib.moe_clip_grads(T(), T(dtype=0), 1, 1.0, p, p, n, None) == INV
+
+
+def _shape(**kw):
+    base = dict(T=4, d=128, n_experts=8, inter=64, top_k=2, n_shared=1, inter_shared=64, has_bias=1, dtype=moe.MOE_BF16,
+                gate_mode=0, routed_fmt=moe.FMT_NATIVE)
+    base.update(kw)
+    return moe.MoeShape(*[base[f] for f, _ in moe.MoeShape._fields_])
+
+
+def test_few_sizes_and_workspace():
+    n = moe.few_workspace_bytes(_shape())
+    assert n > 0 and moe.few_workspace_bytes(_shape(T=16)) > n and moe.few_workspace_bytes(_shape(T=0)) > 0
+    assert moe.few_workspace_bytes(_shape(T=1)) < n             # one workspace for fewer tokens, too
+    for bad in (dict(T=17), dict(d=32776), dict(d=132), dict(T=-1), dict(top_k=9), dict(dtype=moe.MOE_F32, d=130),
+                dict(dtype=moe.MOE_F32, inter=66), dict(dtype=moe.MOE_F32, inter_shared=65),
+                dict(routed_fmt=moe.FMT_MXFP8, d=136), dict(routed_fmt=moe.FMT_E4M3, dtype=moe.MOE_F32)):
+        assert moe.few_workspace_bytes(_shape(**bad)) == 0, bad
+        with pytest.raises(ValueError):
+            moe.new_few_workspace(_shape(**bad), "cpu")
+    assert moe.few_workspace_bytes(_shape(dtype=moe.MOE_F32, n_shared=0, inter_shared=65)) > 0
+
+
+def test_few_c_entry_point_returns_errors():
+    lib = moe.lib_handle()
+    p, odd = ctypes.c_void_p(1 << 40), ctypes.c_void_p((1 << 40) + 8)
+    w = lambda v=1 << 40, **k: moe.MoeWeights(**{**{n: v for n in ("w1", "b1", "w3", "b3", "w2", "b2")}, **k})  # noqa: E731
+
+    def few(sh=None, x=p, c=p, R=None, S=None, out=p, ws=p, n=1 << 30, **kw):
+        sh = _shape(**kw) if sh is None else sh
+        return lib.moe_layer_forward_few(ctypes.byref(sh), x, c, None, ctypes.byref(w() if R is None else R),
+                                         ctypes.byref(w()) if S is None else S, out, None, None, None, ws, n, None)
+
+    assert few(T=0, x=None, out=None) == moe.MOE_OK
+    for kw in (dict(x=None), dict(c=None), dict(out=None), dict(x=odd), dict(c=odd), dict(out=odd), dict(R=w((1 << 40) + 8)),
+               dict(R=w(b1=None)), dict(R=w(s1=1 << 40, s3=1 << 40, s2=1 << 40)), dict(n_shared=0), dict(gate_mode=3)):
+        assert few(**kw) == moe.MOE_ERR_INVALID_ARG, kw
+    assert few(S=ctypes.POINTER(moe.MoeWeights)()) == moe.MOE_ERR_INVALID_ARG
+    for kw in (dict(T=17), dict(d=32776), dict(d=132), dict(dtype=moe.MOE_F32, d=130)):
+        assert few(**kw) == moe.MOE_ERR_UNSUPPORTED, kw
+    need = moe.few_workspace_bytes(_shape())
+    for kw in (dict(ws=None), dict(ws=odd), dict(n=need - 1)):
+        assert few(**kw) == moe.MOE_ERR_WORKSPACE, kw
+
+
+def test_few_binding_refuses_before_any_call():
+    from fine_grained_mixture_route_b200 import workloads as W
+    cfg = W.scaled(W.CONFIGS["small"], T=4, d=64, n_experts=8, top_k=2, inter=32, inter_shared=32)
+    L = W.make_layer(cfg, "cpu")
+    shape = moe.shape_of(L["x"], L["centroids"], L["routed"], 2, L["shared"])
+    ws = torch.zeros(64, dtype=torch.uint8)
+
+    def call(**kw):
+        a = dict(L, ws=ws)
+        a.update(kw)
+        return moe.layer_forward_few(shape, a["x"], a["centroids"], a["routed"], a["shared"], a["ws"],
+                                     **{k: v for k, v in kw.items() if k in ("out", "gate", "router_bias")})
+
+    with pytest.raises(ValueError, match="CUDA"):
+        call()
+    for kw, what in ((dict(x=L["x"].float()), "x has dtype"), (dict(x=L["x"][:3]), "x holds"), (dict(ws=torch.zeros(8)), "ws"),
+                     (dict(out=torch.zeros(4, 64)), "out"), (dict(gate=torch.zeros(7)), "gate"),
+                     (dict(router_bias=torch.zeros(7)), "router_bias"),
+                     (dict(routed=dict(L["routed"], w2=L["routed"]["w2"].float())), "routed.w2")):
+        with pytest.raises(ValueError, match=what):
+            call(**kw)
