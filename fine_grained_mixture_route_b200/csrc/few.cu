@@ -3,19 +3,24 @@
 //   out[t] = sum over shared and picked experts of w2_e h[e,t], plus the gated b2.
 // With so few rows every weight is used a handful of times, so the layer is bound by reading the
 // matrices of the experts that some token picked, once.  One block per SM streams them through a
-// shared-memory ring by bulk copies, and one producer warp keeps that ring full across all steps:
+// shared-memory ring, and two producer warps keep that ring full across all steps:
 //   router scores (consumers) | shared experts' w1, w3 already arrive, they do not depend on the picks
 //   -> all blocks have written their scores: every block ranks all tokens itself (router warps), while its
 //      consumers work on the shared experts
 //   -> picked experts' w1, w3
 //   -> all blocks have written h: w2, whose first stages arrived while the block waited.
 //
-// Work is cut into units of 16 weight rows over the full contraction: 8 rows of w1 with the same 8 of w3
-// (both halves of the SwiGLU in one thread's registers), or 16 rows of w2.  A unit's stages hold 16 x 2 KB;
-// the 8 consumer warps split a stage's columns and add up at the end of the unit.  Up-projection units go
-// round the blocks; the down-projection's units (output columns x expert) are cut into equal contiguous
-// ranges, so a block may hold part of a column block's experts: it then writes partial sums, and the block
-// that completes a column block adds them in block order.  Nothing depends on timing but who does that.
+// Work is cut into units of 16 or 32 weight rows over the full contraction: in each row tile of 16, 8 rows of
+// w1 with the same 8 of w3 (both halves of the SwiGLU in one thread's registers), or 16 rows of w2.  A unit's
+// stages hold a slice of its columns, of the weights and of its tokens' activations alike; the 8 consumer warps
+// split the slice and add up at the end of the unit.  Up-projection units go round the blocks; the
+// down-projection's units (output columns x expert) are cut into equal contiguous ranges, so a block may hold
+// part of a column block's experts: it then writes partial sums, and the block that completes a column block
+// adds them in block order.  Nothing depends on timing but who does that.
+//
+// The ring is filled by cp.async, 16 bytes a thread: bulk copies cost about 30 ns each however short (rows of
+// 1 KB: 3.7 TB/s, 2 KB: 5.2 TB/s; cp.async: 6.1 to 6.4 TB/s for either, measured with nothing else in the
+// kernel).  Activations take the same way, as loads straight into registers would be waited for at every slice.
 //
 // Products: mma.sync m16n8k16 with the weights as the 16-row operand and the tokens as the 8 columns, fp32
 // accumulators.  tcgen05's smallest tile is 64 or 128 weight rows, too coarse to spread a few experts evenly
@@ -37,27 +42,33 @@ namespace {
 
 constexpr int CONS_WARPS = 8;
 constexpr int CONS = CONS_WARPS * 32;
-constexpr int ROUTE_WARPS = 3;                               // 12 warps in all: 168 registers a thread
-constexpr int PRODUCER = CONS_WARPS;                            // warp index
-constexpr int THREADS = CONS + 32 + ROUTE_WARPS * 32;
-constexpr int ROW_BYTES = 2048;                                 // of one weight row in a stage
-constexpr int ROWS = 16;
-constexpr int STAGE_BYTES = ROWS * (ROW_BYTES + 64);
-constexpr int MAX_STAGES = 6;
+constexpr int ROUTE_WARPS = 2, PRODUCERS = 2;                   // 12 warps in all: 168 registers a thread
+constexpr int THREADS = CONS + (ROUTE_WARPS + PRODUCERS) * 32;
+constexpr int MAX_STAGES = 8;
+constexpr int RING_BYTES = 128 << 10;                           // of weights under way that are enough
 constexpr int SMEM_LIMIT = 232448;
 
 enum { W_F32, W_BF16, W_E4M3, W_MX };
 
-// esz: bytes of a weight.  PITCH: of a row in a stage, so that the fragment loads of 8 rows (16 bytes a
-// thread) or 4 rows (8 bytes a thread) fall into different banks.  A slice is what the 8 warps take at
-// once: 128 columns each (fp32: 64).
-template <int F>
+// A stage: 16 R weight rows (R row tiles) over KS columns, the same columns of the unit's tokens, and with block
+// scales the rows' scale bytes.  FR: format of the routed experts, F: of these weights.  The 8 consumer warps
+// take KS / 8 columns each.  PITCH, ACT: of a weight row and an activation row, so that the fragment loads of 8
+// rows (16 bytes a thread) or 4 rows (8 bytes a thread) fall into different banks.
+template <int FR, int F>
 struct Fmt {
     static constexpr int esz = F == W_F32 ? 4 : F == W_BF16 ? 2 : 1;
-    static constexpr int KS = ROW_BYTES / esz;
-    static constexpr int PITCH = ROW_BYTES + (esz == 1 ? 32 : 64);
-    static constexpr int PER_WARP = F == W_F32 ? 64 : 128;
-    static constexpr int SLICE = PER_WARP * CONS_WARPS;
+    static constexpr int ROWB = FR == W_F32 || FR == W_BF16 ? 1024 : 512;
+    static constexpr int KS = ROWB / esz;
+    static constexpr int PITCH = ROWB + (esz == 1 ? 32 : 64);
+    static constexpr int PER_WARP = KS / CONS_WARPS;
+};
+constexpr int ACT = 1024 + 64;                                  // 512 bf16 or 256 fp32 columns
+template <int FR, int R>
+struct Stage {
+    static constexpr int HL = FR == W_F32 ? 1 : 2;              // parts of an activation row
+    static constexpr int acts = 16 * R * (Fmt<FR, FR>::ROWB + 64);
+    static __host__ __device__ int scales(int T) { return acts + T * HL * ACT; }
+    static __host__ __device__ int bytes(int T) { return scales(T) + (FR == W_MX ? 16 * R * 16 : 0); }
 };
 
 struct Params {
@@ -70,40 +81,52 @@ struct Params {
     int32_t* counts;
     float* logits;                                              // [T][E]
     void* h;                                                    // bf16 [rows][2][Hs] (high, low part), fp32 [rows][Hs]
-    float4* part;                                               // [blocks][2][NT][32]
-    unsigned* cnt;                                              // [column blocks][NT]: units already added up
+    float4* part;                                               // [blocks][2][R NT][32]
+    unsigned* cnt;                                              // [column blocks][R NT]: units already added up
     uint32_t* err;
     unsigned long long* bar;                                    // two grid barriers (arrivals, ever growing)
-    int T, d, E, I, k, Ks, Is, Hs, mode, nst;
+    int T, d, E, I, k, Ks, Is, Hs, mode, nst, stage;
     bool bias;
 };
 
 // Dynamic shared memory, in bytes from its start.
+constexpr int SPARE = ROUTE_WARPS * 4;                          // groups of 8 lanes that rank tokens
 struct Smem {
-    int ring, bars, red, mask, base, ge, gm, gb, gates, zl, pidx, pgate, misc, total;
-    __host__ __device__ Smem(int nst, int NT, int T, int E, int k) {
+    int ring, bars, turns, red, mask, base, ge, gm, gb, gates, pidx, pgate, misc, total;
+    __host__ __device__ Smem(int ring_bytes, int frags, int T, int E, int k) {
         const int groups = E < T * k ? E : T * k;
         int o = 0;
         auto take = [&](int bytes) { const int at = o; o += (bytes + 15) / 16 * 16; return at; };
-        ring = take(nst * STAGE_BYTES);
-        bars = take((2 * MAX_STAGES + 1) * 8);
-        red = take(2 * CONS_WARPS * NT * 32 * 16);
+        ring = take(ring_bytes);
+        bars = take((2 * MAX_STAGES + 3) * 8);
+        turns = take(2 * 8);
+        red = take(2 * CONS_WARPS * frags * 32 * 16);
         mask = take(E * 4);
         base = take(E * 4);
         ge = take(groups * 4);
         gm = take(groups * 4);
         gb = take(groups * 4);
         gates = take(T * k * 4);
-        zl = take(ROUTE_WARPS * E * 4);
-        pidx = take(T * k * 4);
-        pgate = take(T * k * 4);
+        pidx = take((T + SPARE) * k * 4);
+        pgate = take((T + SPARE) * k * 4);
         misc = take(16);
         total = o;
     }
 };
 
 __device__ __forceinline__ void named_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-__device__ __forceinline__ void named_arrive(int id, int n) { asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+// Asynchronous copies of 16 bytes past the L1, or of 4 (both addresses aligned to them), and the arrival of all
+// of a thread's copies so far on a barrier that counts its threads.
+template <int N>
+__device__ __forceinline__ void async_load(uint32_t dst, const void* src) {
+    if (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -113,31 +136,39 @@ __device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Four e4m3 codes as two bf16 pairs (exact; NaN stays NaN).
+// Four e4m3 codes as two bf16 pairs (exact; NaN stays NaN): the upper halves of the fp32 values, picked by bytes,
+// as conversions that round run at a fraction of the rate.
 __device__ __forceinline__ uint2 bf16_of_codes(uint32_t w) {
     uint32_t o[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-        o[i] = *reinterpret_cast<const uint32_t*>(&b);
+        o[i] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
     }
     return make_uint2(o[0], o[1]);
 }
 
 __device__ __forceinline__ float scale_of_byte(uint32_t b) { return __uint_as_float(b ? b << 23 : 0x00400000u); }
 
-// Arrival number `old` (of G per round) on a barrier that only grows: the count that completes its round.
-__device__ __forceinline__ unsigned long long round_end(unsigned long long old, unsigned G) { return (old / G + 1) * G; }
+// A grid barrier is a count of arrivals, G per round, that only grows: round_end is the count that completes the
+// round in which it stands at `v`.
+__device__ __forceinline__ unsigned long long load_acquire(const unsigned long long* p) {
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned long long round_end(unsigned long long v, unsigned G) { return (v / G + 1) * G; }
+__device__ __forceinline__ void grid_arrive(unsigned long long* bar) {
+    __threadfence();
+    asm volatile("red.release.gpu.global.add.u64 [%0], 1;" ::"l"(bar) : "memory");
+}
 
 __device__ __forceinline__ bool grid_wait(unsigned long long* bar, unsigned long long target, volatile int* abort_flag,
                                           uint32_t* err) {
-    unsigned long long v;
     const unsigned long long t0 = globaltimer();
     for (uint32_t i = 1;; ++i) {
-        asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(bar) : "memory");
-        if (v >= target) return true;
+        if (load_acquire(bar) >= target) return true;
         if ((i & 63u) == 0u) {
             if (*abort_flag) return false;
             if (globaltimer() - t0 > WAIT_NS || i >= WAIT_MAX_POLLS) {
@@ -152,45 +183,24 @@ __device__ __forceinline__ bool grid_wait(unsigned long long* bar, unsigned long
 // A block's place in the ring: the producer and the consumers count the same stages.
 struct Ring {
     uint32_t base, bars;
-    int nst, slot;
+    int nst, stage, slot;
     uint32_t phase;
     __device__ __forceinline__ uint32_t full() const { return bars + slot * 8; }
     __device__ __forceinline__ uint32_t empty() const { return bars + (MAX_STAGES + slot) * 8; }
-    __device__ __forceinline__ uint32_t at() const { return base + slot * STAGE_BYTES; }
+    __device__ __forceinline__ uint32_t at() const { return base + slot * stage; }
     __device__ __forceinline__ void next() {
         if (++slot == nst) { slot = 0; phase ^= 1u; }
     }
 };
 
-// A thread's activation fragments of one slice: 4 steps of 32 columns, 8 columns a thread, for the token
-// of its fragment column in each group of 8 tokens; HL = 2: high and low parts.  sf: the scale bytes of the
-// warp's 4 runs for its two weight rows.
-template <int NT, int HL>
-struct Act {
-    uint4 v[HL][NT][4];
-    uint32_t sf[2];
-};
-
-template <int NT, int HL>
-__device__ __forceinline__ void load_act(Act<NT, HL>& b, const __nv_bfloat16* const (&ptr)[NT], int low, int kb, int K,
-                                         int lane) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int k = kb + s * 32 + (lane & 3) * 8;
-            const bool in = ptr[nt] != nullptr && k < K;
-#pragma unroll
-            for (int q = 0; q < HL; ++q)
-                b.v[q][nt][s] = !in ? make_uint4(0, 0, 0, 0)
-                                    : HL == 1 ? __ldg(reinterpret_cast<const uint4*>(ptr[nt] + k))
-                                              : __ldcg(reinterpret_cast<const uint4*>(ptr[nt] + q * low + k));
-        }
-}
-
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
     return v;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -199,50 +209,65 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
-// acc += 16 weight rows x up to 8 NT tokens over the warp's 128 columns kb .. of a slice that starts at byte
-// `off` of each row in the stage.  Columns past K hold an earlier stage's bytes: both operands are zeroed.
-template <int F, int NT, int HL>
-__device__ __forceinline__ void mma_slice(float (&acc)[NT * 4], const Act<NT, HL>& b, uint32_t stage, int off, int kb,
-                                          int K, uint32_t mask, int lane) {
+// acc += 16 R weight rows x up to 8 NT tokens over the warp's columns kb .. < K of a stage, wk columns from its
+// start.  act[nt]: the thread's token's row in the stage (0: the token is not among the unit's); HL = 2: its low
+// part follows `low` bytes on.  Columns past K hold an earlier stage's bytes: both operands are zeroed.
+template <int FR, int F, int NT, int HL, int R>
+__device__ __forceinline__ void mma_stage(float (&acc)[R][NT * 4], uint32_t stage, const uint32_t (&act)[NT], int low,
+                                          uint32_t sfs, int wk, int kb, int K, uint32_t mask, int lane) {
+    using L = Fmt<FR, F>;
     const int g = lane >> 2, c = (lane & 3) * 8;
-    const uint32_t row = stage + g * Fmt<F>::PITCH + off;
+    const uint32_t row = stage + g * L::PITCH;
+    uint32_t sf[R][2];
+    if (F == W_MX) {                                            // 2 runs of 64 columns
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        uint4 a0 = make_uint4(0, 0, 0, 0), a1 = make_uint4(0, 0, 0, 0);
-        if (kb + s * 32 + c < K) {
-            if (F == W_BF16) {
-                a0 = lds128(row + (s * 32 + c) * 2);
-                a1 = lds128(row + 8 * Fmt<F>::PITCH + (s * 32 + c) * 2);
-            } else {
-                const uint2 q0 = lds64(row + s * 32 + c), q1 = lds64(row + 8 * Fmt<F>::PITCH + s * 32 + c);
-                const uint2 l0 = bf16_of_codes(q0.x), h0 = bf16_of_codes(q0.y);
-                const uint2 l1 = bf16_of_codes(q1.x), h1 = bf16_of_codes(q1.y);
-                a0 = make_uint4(l0.x, l0.y, h0.x, h0.y);
-                a1 = make_uint4(l1.x, l1.y, h1.x, h1.y);
-            }
-        }
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (NT > 1 && ((mask >> (8 * nt)) & 0xFFu) == 0u) continue;
-            if (F == W_MX) {                                    // a run's own sum, scaled in fp32
-                float t[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int h = 0; h < 2; ++h)
+                sf[i][h] = lds32(sfs + (i * 16 + h * 8 + g) * 16 + wk / 128 * 4) >> (wk / 64 % 2 * 16);
+    }
 #pragma unroll
-                for (int q = 0; q < HL; ++q) {
-                    const uint4& v = b.v[q][nt][s];
-                    mma_bf16(t, a0.x, a1.x, a0.y, a1.y, v.x, v.y);
-                    mma_bf16(t, a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+    for (int s = 0; s < L::PER_WARP / 32; ++s) {
+        const int k = wk + s * 32 + c;
+        const bool in = kb + s * 32 + c < K;
+        uint4 b[NT][HL];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int q = 0; q < HL; ++q)
+                b[nt][q] = in && act[nt] ? lds128(act[nt] + q * low + k * 2) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const uint32_t at = row + i * 16 * L::PITCH + k * L::esz;
+            uint4 a0 = make_uint4(0, 0, 0, 0), a1 = make_uint4(0, 0, 0, 0);
+            if (in) {
+                if (F == W_BF16) {
+                    a0 = lds128(at);
+                    a1 = lds128(at + 8 * L::PITCH);
+                } else {
+                    const uint2 q0 = lds64(at), q1 = lds64(at + 8 * L::PITCH);
+                    const uint2 l0 = bf16_of_codes(q0.x), h0 = bf16_of_codes(q0.y);
+                    const uint2 l1 = bf16_of_codes(q1.x), h1 = bf16_of_codes(q1.y);
+                    a0 = make_uint4(l0.x, l0.y, h0.x, h0.y);
+                    a1 = make_uint4(l1.x, l1.y, h1.x, h1.y);
                 }
-                const float f0 = scale_of_byte((b.sf[0] >> (8 * s)) & 0xFFu), f1 = scale_of_byte((b.sf[1] >> (8 * s)) & 0xFFu);
-                acc[nt * 4] = fmaf(t[0], f0, acc[nt * 4]);
-                acc[nt * 4 + 1] = fmaf(t[1], f0, acc[nt * 4 + 1]);
-                acc[nt * 4 + 2] = fmaf(t[2], f1, acc[nt * 4 + 2]);
-                acc[nt * 4 + 3] = fmaf(t[3], f1, acc[nt * 4 + 3]);
-            } else {
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                if (NT > 1 && ((mask >> (8 * nt)) & 0xFFu) == 0u) continue;
+                float t[4] = {0.f, 0.f, 0.f, 0.f};              // block scales: a run's own sum, scaled in fp32
+                float* to = F == W_MX ? t : acc[i] + nt * 4;
 #pragma unroll
                 for (int q = 0; q < HL; ++q) {
-                    const uint4& v = b.v[q][nt][s];
-                    mma_bf16(acc + nt * 4, a0.x, a1.x, a0.y, a1.y, v.x, v.y);
-                    mma_bf16(acc + nt * 4, a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+                    mma_bf16(to, a0.x, a1.x, a0.y, a1.y, b[nt][q].x, b[nt][q].y);
+                    mma_bf16(to, a0.z, a1.z, a0.w, a1.w, b[nt][q].z, b[nt][q].w);
+                }
+                if (F == W_MX) {
+                    const float f0 = scale_of_byte((sf[i][0] >> (8 * s)) & 0xFFu), f1 = scale_of_byte((sf[i][1] >> (8 * s)) & 0xFFu);
+                    acc[i][nt * 4] = fmaf(t[0], f0, acc[i][nt * 4]);
+                    acc[i][nt * 4 + 1] = fmaf(t[1], f0, acc[i][nt * 4 + 1]);
+                    acc[i][nt * 4 + 2] = fmaf(t[2], f1, acc[i][nt * 4 + 2]);
+                    acc[i][nt * 4 + 3] = fmaf(t[3], f1, acc[i][nt * 4 + 3]);
                 }
             }
         }
@@ -257,80 +282,81 @@ struct Me {
     uint32_t* err;
 };
 
-__device__ __forceinline__ void wait_full(Me& me) { mbar_wait(me.ring.full(), me.ring.phase, me.abort_flag, me.err); }
+__device__ __forceinline__ void wait_full(Me& me) {
+    mbar_wait_limit(me.ring.full(), me.ring.phase, me.abort_flag, me.err, true, WAIT_NS);
+}
 __device__ __forceinline__ void release(Me& me) {
     __syncwarp();
     if (me.lane == 0) mbar_arrive(me.ring.empty());
     me.ring.next();
 }
 
-// One unit of 16 rows on the tensor cores.  ptr: the thread's tokens' activation rows (NULL: not among the
-// unit's); sfw[q] (block scales): the words of the runs' scale bytes of the thread's two rows, one per 128
-// columns, 1 KB apart.
-template <int F, int NT, int HL>
-__device__ __forceinline__ void unit_mma(float (&acc)[NT * 4], Me& me, const __nv_bfloat16* const (&ptr)[NT], int low, int K,
-                                         uint32_t mask, const uint8_t* const (&sfw)[2]) {
-    constexpr int SUBS = Fmt<F>::KS / Fmt<F>::SLICE;
-    const int wk = me.warp * Fmt<F>::PER_WARP;
-    Act<NT, HL> b;
-    auto load = [&](int k0) {
-        const int kb = k0 + wk;
-        load_act<NT, HL>(b, ptr, low, kb, K, me.lane);
-        if (F == W_MX && kb < K) {
-            b.sf[0] = __ldg(reinterpret_cast<const uint32_t*>(sfw[0] + (size_t)(kb / 128) * 1024));
-            b.sf[1] = __ldg(reinterpret_cast<const uint32_t*>(sfw[1] + (size_t)(kb / 128) * 1024));
-        }
-    };
-    load(0);
-    for (int k0 = 0; k0 < K;) {
-        wait_full(me);
-        const uint32_t stage = me.ring.at();
+// One unit of 16 R rows on the tensor cores for the tokens of `mask`, whose activation rows stand in each stage
+// in order, with HL parts each.
+template <int FR, int F, int NT, int HL, int R>
+__device__ __forceinline__ void unit_mma(float (&acc)[R][NT * 4], Me& me, int sfs, int K, uint32_t mask) {
+    using L = Fmt<FR, F>;
+    const int wk = me.warp * L::PER_WARP;
+    int act[NT];
 #pragma unroll
-        for (int sub = 0; sub < SUBS; ++sub) {
-            if (k0 >= K) break;
-            if (k0 + wk < K)
-                mma_slice<F, NT, HL>(acc, b, stage, (sub * Fmt<F>::SLICE + wk) * Fmt<F>::esz, k0 + wk, K, mask, me.lane);
-            k0 += Fmt<F>::SLICE;
-            if (k0 < K) load(k0);
+    for (int nt = 0; nt < NT; ++nt) {
+        const int n = nt * 8 + (me.lane >> 2);
+        act[nt] = (mask >> n) & 1u ? Stage<FR, R>::acts + __popc(mask & ((1u << n) - 1u)) * HL * ACT : 0;
+    }
+    for (int k0 = 0; k0 < K; k0 += L::KS) {
+        wait_full(me);
+        if (k0 + wk < K) {
+            const uint32_t stage = me.ring.at();
+            uint32_t a[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) a[nt] = act[nt] ? stage + act[nt] : 0u;
+            mma_stage<FR, F, NT, HL, R>(acc, stage, a, ACT, stage + sfs, wk, k0 + wk, K, mask, me.lane);
         }
         release(me);
     }
 }
 
 // One unit of 16 rows in fp32: lane pairs share a row, each lane every other 16-byte piece of the warp's
-// 64 columns, and acc[n] is token n's sum.
+// 32 columns, and acc[n] is token n's sum.
 template <int NT>
-__device__ __forceinline__ void unit_f32(float (&acc)[NT * 8], Me& me, const float* const (&ptr)[NT * 8], int K) {
+__device__ __forceinline__ void unit_f32(float (&acc)[NT * 8], Me& me, int K, uint32_t mask) {
+    using L = Fmt<W_F32, W_F32>;
     const int row = me.lane >> 1, half = me.lane & 1;
-    for (int k0 = 0; k0 < K; k0 += Fmt<W_F32>::KS) {
+    for (int k0 = 0; k0 < K; k0 += L::KS) {
         wait_full(me);
-        const uint32_t a = me.ring.at() + row * Fmt<W_F32>::PITCH;
+        const uint32_t a = me.ring.at() + row * L::PITCH, x = me.ring.at() + Stage<W_F32, 1>::acts;
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const int c = me.warp * 64 + (q * 2 + half) * 4;
+        for (int q = 0; q < 4; ++q) {
+            const int c = me.warp * L::PER_WARP + (q * 2 + half) * 4;
             if (k0 + c >= K) continue;
             const uint4 u = lds128(a + c * 4);
             const float w0 = __uint_as_float(u.x), w1 = __uint_as_float(u.y), w2 = __uint_as_float(u.z),
                         w3 = __uint_as_float(u.w);
+            uint32_t at = x + c * 4;
 #pragma unroll
             for (int n = 0; n < NT * 8; ++n) {
-                if (!ptr[n]) continue;
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(ptr[n] + k0 + c));
-                acc[n] = fmaf(w0, v.x, fmaf(w1, v.y, fmaf(w2, v.z, fmaf(w3, v.w, acc[n]))));
+                if (!((mask >> n) & 1u)) continue;
+                const uint4 v = lds128(at);
+                at += ACT;
+                acc[n] = fmaf(w0, __uint_as_float(v.x),
+                              fmaf(w1, __uint_as_float(v.y), fmaf(w2, __uint_as_float(v.z), fmaf(w3, __uint_as_float(v.w), acc[n]))));
             }
         }
         release(me);
     }
 }
 
-// The 8 warps' fragments of a unit to shared memory; after the barrier, warp (turn * NT + nt) % 8 holds the
-// sums of token group nt in fragment order: c[0], c[1]: weight row lane / 4, tokens 2 (lane % 4) and + 1;
+// The 8 warps' fragments of a unit to shared memory.  Fragment f = row tile * NT + group of 8 tokens; after the
+// barrier one warp adds up a fragment: c[0], c[1]: weight row lane / 4 of the tile, tokens 2 (lane % 4) and + 1;
 // c[2], c[3]: row lane / 4 + 8.  The two buffers alternate, so one barrier per unit is enough.
-template <int NT>
-__device__ __forceinline__ void put_frag(float4* red, const float (&acc)[NT * 4], const Me& me) {
+template <int NT, int R>
+__device__ __forceinline__ void put_frag(float4* red, const float (&acc)[R][NT * 4], const Me& me) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-        red[(me.warp * NT + nt) * 32 + me.lane] = make_float4(acc[nt * 4], acc[nt * 4 + 1], acc[nt * 4 + 2], acc[nt * 4 + 3]);
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            red[(me.warp * R * NT + i * NT + nt) * 32 + me.lane] =
+                make_float4(acc[i][nt * 4], acc[i][nt * 4 + 1], acc[i][nt * 4 + 2], acc[i][nt * 4 + 3]);
 }
 template <int NT>
 __device__ __forceinline__ void put_f32(float4* red, float (&acc)[NT * 8], const Me& me) {
@@ -342,15 +368,100 @@ __device__ __forceinline__ void put_f32(float4* red, float (&acc)[NT * 8], const
             reinterpret_cast<float*>(red + (me.warp * NT + n / 8) * 32 + (row & 7) * 4 + (n & 7) / 2)[(row >> 3) * 2 + (n & 1)] = t;
     }
 }
-template <int NT>
-__device__ __forceinline__ float4 take_frag(const float4* red, int nt, int lane) {
-    float4 t = red[nt * 32 + lane];
+template <int FRAGS>
+__device__ __forceinline__ float4 take_frag(const float4* red, int f, int lane) {
+    float4 t = red[f * 32 + lane];
 #pragma unroll
     for (int w = 1; w < CONS_WARPS; ++w) {
-        const float4 v = red[(w * NT + nt) * 32 + lane];
+        const float4 v = red[(w * FRAGS + f) * 32 + lane];
         t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
     }
     return t;
+}
+
+// Picks and gates of one token by W lanes (l: a lane's place among them) from its E <= W NPL logits zg: the rules
+// of warp_route, made for latency.  A lane keeps the keys of its experts l + W i in registers, in an unsigned
+// order (0: none left; taken, NaN or -infinity), and every round is one search of the lane's own keys and one
+// reduction (largest key, lowest index that has it).  Gates wait: the picks are what the weights' copies need.
+__device__ __forceinline__ float key_of(float z, int e, int mode, const float* __restrict__ bias) {
+    const float b = bias ? bias[e] : 0.f;
+    return mode == 2 ? 1.0f / (1.0f + expf(-z)) + b : z + b;
+}
+template <int W, int NPL>
+__device__ __forceinline__ void few_pick(const float* zg, int E, int k, int mode, const float* __restrict__ bias, int l,
+                                         int32_t* idx_row, float* key_row) {
+    float v[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) v[i] = l + W * i < E ? __ldcg(zg + l + W * i) : 0.f;
+    uint32_t key[NPL];
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) {
+        const float y = l + W * i < E ? key_of(v[i], l + W * i, mode, bias) : -INFINITY;
+        const uint32_t b = __float_as_uint(y + 0.f);            // the two zeros are equal
+        key[i] = y > -INFINITY ? (b >> 31 ? ~b : b | 0x80000000u) : 0u;
+    }
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = 0u;
+        int at = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (key[i] > best) { best = key[i]; at = l + W * i; }
+        if (W == 32) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+            at = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7fffffff);
+            best = top;
+        } else {
+#pragma unroll
+            for (int o = W / 2; o > 0; o >>= 1) {
+                const uint32_t ob = __shfl_xor_sync(0xffffffffu, best, o);
+                const int oa = __shfl_xor_sync(0xffffffffu, at, o);
+                if (ob > best || (ob == best && oa < at)) { best = ob; at = oa; }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (l + W * i == at) key[i] = 0u;
+        if (l == 0) {
+            idx_row[j] = at;
+            key_row[j] = best == 0u ? -INFINITY : __uint_as_float(best >> 31 ? best & 0x7FFFFFFFu : ~best);
+        }
+    }
+    __syncwarp();
+}
+// gate_row: the picks' keys as few_pick left them, and in the end the gates.
+template <int W, int NPL>
+__device__ __forceinline__ void few_gate(const float* zg, int E, int k, int mode, const float* __restrict__ bias, int l,
+                                         const int32_t* idx_row, float* gate_row) {
+    auto sum = [](float v) {
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    };
+    float m = -INFINITY, s = 0.f;
+    if (mode == 0) {
+        float v[NPL];
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            v[i] = l + W * i < E ? key_of(__ldcg(zg + l + W * i), l + W * i, 0, bias) : -INFINITY;
+            m = fmaxf(m, v[i]);
+        }
+#pragma unroll
+        for (int o = W / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+        for (int i = 0; i < NPL; ++i)
+            if (l + W * i < E) s += expf(v[i] - m);
+    } else if (mode == 1) {
+        m = gate_row[0];
+    }
+    __syncwarp();
+    for (int j = l; j < k; j += W) {
+        const float g = mode == 2 ? 1.0f / (1.0f + expf(-__ldcg(zg + (idx_row[j] < E ? idx_row[j] : 0)))) : expf(gate_row[j] - m);
+        gate_row[j] = g;
+        if (mode != 0) s += g;
+    }
+    s = 1.0f / sum(s);
+    for (int j = l; j < k; j += W) gate_row[j] *= s;
+    __syncwarp();
 }
 
 // One expert as a unit sees it.
@@ -361,8 +472,10 @@ struct Group {
     bool shared;
 };
 
-template <int FR, int NT>
+template <int FR, int NT, int R>
 struct Kernel {
+    static_assert(FR != W_F32 || R == 1, "fp32 units have one row tile");
+    static constexpr int FRAGS = R * NT, UP = 8 * R, DOWN = 16 * R;    // fragments, rows of w1 (and w3) and of w2 of a unit
     static constexpr int FS = FR == W_F32 ? W_F32 : W_BF16;
     using T = typename std::conditional<FR == W_F32, float, __nv_bfloat16>::type;
 
@@ -371,13 +484,15 @@ struct Kernel {
     const Smem L;
     const int G;                                                // blocks
 
-    __device__ Kernel(const Params& p_, char* sm_) : p(p_), sm(sm_), L(p_.nst, NT, p_.T, p_.E, p_.k), G((int)gridDim.x) {}
+    __device__ Kernel(const Params& p_, char* sm_) : p(p_), sm(sm_), L(p_.nst * p_.stage, FRAGS, p_.T, p_.E, p_.k), G((int)gridDim.x) {}
     template <typename U>
     __device__ __forceinline__ U* at(int off) const { return reinterpret_cast<U*>(sm + off); }
     __device__ __forceinline__ volatile int* abort_flag() const { return at<int>(L.misc); }
     __device__ __forceinline__ int n_routed() const { return at<volatile int>(L.misc)[1]; }
     __device__ __forceinline__ uint32_t route_bar() const { return smem_u32(sm + L.bars) + 2 * MAX_STAGES * 8; }
-    __device__ __forceinline__ Ring ring() const { return Ring{smem_u32(sm + L.ring), smem_u32(sm + L.bars), p.nst, 0, 0}; }
+    __device__ __forceinline__ uint32_t h_bar() const { return route_bar() + 8; }
+    __device__ __forceinline__ uint32_t gate_bar() const { return route_bar() + 16; }
+    __device__ __forceinline__ Ring ring() const { return Ring{smem_u32(sm + L.ring), smem_u32(sm + L.bars), p.nst, p.stage, 0, 0}; }
 
     __device__ __forceinline__ Group group(int gi) const {      // shared experts first
         Group q;
@@ -396,144 +511,275 @@ struct Kernel {
         return q;
     }
     // units of the up-projection: shared ones, then (picks known) the routed experts'
-    __device__ __forceinline__ int shared_units() const { return p.Ks * ceil_div(p.Is, 8); }
+    __device__ __forceinline__ int shared_units() const { return p.Ks * ceil_div(p.Is, UP); }
     __device__ __forceinline__ void up_unit(int u, Group& q, int& r0) const {
-        const int su = shared_units(), b = u < su ? ceil_div(p.Is, 8) : ceil_div(p.I, 8);
+        const int su = shared_units(), b = u < su ? ceil_div(p.Is, UP) : ceil_div(p.I, UP);
         const int v = u < su ? u : u - su;
         q = group((u < su ? 0 : p.Ks) + v / b);
-        r0 = v % b * 8;
+        r0 = v % b * UP;
     }
-    // the down-projection's range of block c among U units
-    __device__ __forceinline__ int down_start(long long U, int c) const { return (int)(U * c / G); }
+    // the down-projection's range of block c among U units (U G < 2^32: at most 2048 column blocks of 576 groups)
+    __device__ __forceinline__ int down_start(uint32_t U, int c) const { return (int)(U * (uint32_t)c / (uint32_t)G); }
+    // the block whose range holds unit u: the last c with U c < (u + 1) G
+    __device__ __forceinline__ int down_block(uint32_t U, int u) const { return (int)(((uint32_t)(u + 1) * (uint32_t)G - 1u) / U); }
 
-    // ------------------------------------------------------------------------------ producer
-    __device__ void produce() {
+    // ------------------------------------------------------------------------------ producers
+    // What a unit's stages bring, column by column: weights, then activations.  Warp w of the two copies the first
+    // (0) or second 8 rows of each row tile (w1 and w3 of an up unit), and every other activation row; warp 0
+    // copies the scale bytes.  A warp keeps its rows' addresses: 5 instructions a row and stage, as every one
+    // delays the next copy.  Rows behind the matrix repeat its last one; their sums are not used.
+    struct Source {
+        const char* row[8 * R];                                 // this lane's 16 bytes of the first stage
+        int bytes, esz;                                         // of a weight row, of a weight
+        const char* act;                                        // activations of the unit's first token, this lane's part
+        int act_row, act_low;                                   // bytes between tokens' rows, and to the low part (0: none)
+        uint32_t mask;
+        bool by_token;                                          // rows of x: by token; of h: in order
+        const char* sf;                                         // this lane's row's scale word of the first 128 columns
+        // row j of tile i: row i * tile + j of the matrix at `at`, of which `there` rows are left
+        __device__ __forceinline__ void rows(const void* at, int tile, int there, int lane) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int r = i * tile + j < there ? i * tile + j : there - 1;
+                    row[i * 8 + j] = static_cast<const char*>(at) + (long long)r * bytes + lane * 16;
+                }
+        }
+    };
+    __device__ __forceinline__ void copy_weights(const Source& q, const Ring& ring, int c, int w, int lane) const {
+        constexpr int ROWB = Fmt<FR, FR>::ROWB;
+        const int to = ROWB + (q.esz == 1 ? 32 : 64);
+        uint32_t dst = ring.at() + w * 8 * to + lane * 16;
+        const bool in0 = c + lane * 16 < q.bytes, in1 = ROWB > 512 && c + 512 + lane * 16 < q.bytes;
+#pragma unroll
+        for (int i = 0; i < R; ++i, dst += 8 * to)
+#pragma unroll
+            for (int j = 0; j < 8; ++j, dst += to) {
+                const char* src = q.row[i * 8 + j] + c;
+                if (in0) async_load<16>(dst, src);
+                if (in1) async_load<16>(dst + 512, src + 512);
+            }
+        if (FR == W_MX && q.sf && w == 0) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (c + j * 128 < q.bytes)
+                    async_load<4>(ring.at() + Stage<FR, R>::scales(p.T) + lane * 16 + j * 4, q.sf + (size_t)(c / 128 + j) * 1024);
+        }
+    }
+    __device__ __forceinline__ void copy_acts(const Source& q, const Ring& ring, int c, int w, int lane) const {
+        const int up = q.esz == 1 ? 1 : 0, c0 = c << up, end = q.bytes << up;    // 8-bit weights have 16-bit activations
+        const bool in0 = c0 + lane * 16 < end, in1 = (Fmt<FR, FR>::ROWB << up) > 512 && c0 + 512 + lane * 16 < end;
+        uint32_t dst = ring.at() + Stage<FR, R>::acts + lane * 16 + w * ACT;
+        const char* a = q.act + c0;
+        auto copy = [&](const char* src) {
+            if (in0) async_load<16>(dst, src);
+            if (in1) async_load<16>(dst + 512, src + 512);
+            dst += 2 * ACT;
+        };
+        if (q.act_low) {                                        // this warp: one part of all rows
+            a += w * q.act_low;
+            for (int n = __popc(q.mask); n > 0; --n, a += q.act_row) copy(a);
+        } else if (!q.by_token) {
+            a += w * q.act_row;
+            for (int n = __popc(q.mask) - w; n > 0; n -= 2, a += 2 * q.act_row) copy(a);
+        } else {
+            uint32_t m = w ? q.mask & (q.mask - 1u) : q.mask;
+            while (m) {
+                copy(a + (size_t)(__ffs(m) - 1) * q.act_row);
+                m &= m - 1u;
+                m &= m - 1u;
+            }
+        }
+    }
+    __device__ __forceinline__ Source up_source(int u, int w, int lane) const {
+        Group g;
+        int r0;
+        up_unit(u, g, r0);
+        const int F = g.shared ? FS : FR, I = g.shared ? p.Is : p.I;
+        const int esz = F == W_F32 ? 4 : F == W_BF16 ? 2 : 1;
+        const void* m = g.shared ? (w ? p.Sh.w3 : p.Sh.w1) : (w ? p.R.w3 : p.R.w1);
+        Source q;
+        q.bytes = p.d * esz; q.esz = esz;
+        q.rows(static_cast<const char*>(m) + ((size_t)g.e * I + r0) * q.bytes, 8, I - r0, lane);
+        q.act = static_cast<const char*>(p.x) + lane * 16;
+        q.act_row = p.d * (int)sizeof(T); q.act_low = 0;
+        q.mask = g.mask; q.by_token = true; q.sf = nullptr;
+        const int r = r0 + (lane >> 4) * 8 + (lane & 7);        // of the lane's row in the stage
+        if (FR == W_MX && !g.shared && lane < DOWN && r < I)
+            q.sf = reinterpret_cast<const char*>(p.R.sf13) + ((size_t)g.e * ceil_div(I, 128) + r / 128) * ceil_div(p.d, 128) * 1024 +
+                   (lane >> 3 & 1) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+        return q;
+    }
+    __device__ __forceinline__ Source down_source(int u, int groups, int w, int lane) const {
+        const Group g = group(u % groups);
+        const int F = g.shared ? FS : FR, I = g.shared ? p.Is : p.I;
+        const int esz = F == W_F32 ? 4 : F == W_BF16 ? 2 : 1;
+        const int r0 = u / groups * DOWN;
+        const void* m = g.shared ? p.Sh.w2 : p.R.w2;
+        Source q;
+        q.bytes = I * esz; q.esz = esz;
+        q.rows(static_cast<const char*>(m) + ((size_t)g.e * p.d + r0 + w * 8) * q.bytes, 16, p.d - r0 - w * 8, lane);
+        q.act_row = p.Hs * 4;                                   // two bf16 parts, or fp32
+        q.act_low = FR == W_F32 ? 0 : p.Hs * 2;
+        q.act = static_cast<const char*>(p.h) + (size_t)g.row * q.act_row + lane * 16;
+        q.mask = g.mask; q.by_token = false; q.sf = nullptr;
+        const int r = r0 + lane;
+        if (FR == W_MX && !g.shared && lane < DOWN && r < p.d)
+            q.sf = reinterpret_cast<const char*>(p.R.sf2) + ((size_t)g.e * ceil_div(p.d, 256) + r / 256) * ceil_div(I, 128) * 1024 +
+                   ((r >> 7) & 1) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+        return q;
+    }
+
+    __device__ void produce(int w) {
+        constexpr int ROWB = Fmt<FR, FR>::ROWB;
         const int lane = threadIdx.x & 31;
         Ring ring = this->ring();
-        long long issued = 0;
-        bool ok = true;
-        // copies the unit's rows (lane's row, or NULL) through the ring
-        auto stream = [&](const char* row, int K, int esz, int pitch) {
-            const int rows = __popc(__ballot_sync(0xffffffffu, row != nullptr));
-            const int KS = ROW_BYTES / esz;
-            for (int k0 = 0; k0 < K; k0 += KS) {
-                ok = mbar_wait(ring.empty(), ring.phase ^ 1u, abort_flag(), p.err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) return;
-                const uint32_t bytes = (uint32_t)(K - k0 < KS ? K - k0 : KS) * esz;
-                if (lane == 0) mbar_expect_tx(ring.full(), rows * bytes);
-                __syncwarp();
-                if (row) bulk_load(ring.at() + lane * pitch, row + (size_t)k0 * esz, bytes, ring.full());
-                ++issued;
-                ring.next();
-            }
+        auto free_slot = [&](const Ring& r) {
+            return __all_sync(0xffffffffu, mbar_try_wait(r.empty(), r.phase ^ 1u) ||
+                                               mbar_wait(r.empty(), r.phase ^ 1u, abort_flag(), p.err)) != 0;
         };
         const int su = shared_units();
         int units = su;
-        bool routed = false;
-        for (int u = blockIdx.x; ok; u += G) {
+        bool routed = false, ok = true;
+        for (int u = blockIdx.x;; u += G) {
             if (u >= units && !routed) {
                 ok = __all_sync(0xffffffffu, mbar_wait(route_bar(), 0, abort_flag(), p.err));
                 routed = true;
-                units = su + n_routed() * ceil_div(p.I, 8);
+                units = su + n_routed() * ceil_div(p.I, UP);
             }
             if (u >= units || !ok) break;
-            Group q;
-            int r0;
-            up_unit(u, q, r0);
-            const int F = q.shared ? FS : FR, I = q.shared ? p.Is : p.I;
-            const int esz = F == W_F32 ? 4 : F == W_BF16 ? 2 : 1;
-            const int r = r0 + (lane & 7);
-            const void* w = q.shared ? (lane < 8 ? p.Sh.w1 : p.Sh.w3) : (lane < 8 ? p.R.w1 : p.R.w3);
-            const char* row = lane < ROWS && r < I ? static_cast<const char*>(w) + ((size_t)q.e * I + r) * p.d * esz : nullptr;
-            stream(row, p.d, esz, ROW_BYTES + (esz == 1 ? 32 : 64));
+            const Source q = up_source(u, w, lane);
+            for (int c = 0; c < q.bytes && (ok = free_slot(ring)); c += ROWB) {
+                copy_weights(q, ring, c, w, lane);
+                copy_acts(q, ring, c, w, lane);
+                async_arrive(ring.full());
+                ring.next();
+            }
         }
         if (ok) {
             const int groups = p.Ks + n_routed();
-            const long long U = (long long)ceil_div(p.d, ROWS) * groups;
-            const int end = down_start(U, blockIdx.x + 1);
-            for (int u = down_start(U, blockIdx.x); u < end && ok; ++u) {
-                const Group q = group(u % groups);
-                const int F = q.shared ? FS : FR, I = q.shared ? p.Is : p.I;
-                const int esz = F == W_F32 ? 4 : F == W_BF16 ? 2 : 1;
-                const int r = u / groups * ROWS + lane;
-                const void* w = q.shared ? p.Sh.w2 : p.R.w2;
-                const char* row = lane < ROWS && r < p.d ? static_cast<const char*>(w) + ((size_t)q.e * p.d + r) * I * esz : nullptr;
-                stream(row, I, esz, ROW_BYTES + (esz == 1 ? 32 : 64));
+            const uint32_t U = (uint32_t)(ceil_div(p.d, DOWN) * groups);
+            const int begin = down_start(U, blockIdx.x), end = down_start(U, blockIdx.x + 1);
+            // weights of as many stages as there are do not wait for h
+            Ring early = ring;
+            int left = p.nst;
+            for (int u = begin; u < end && left > 0 && ok; ++u) {
+                const Source q = down_source(u, groups, w, lane);
+                for (int c = 0; c < q.bytes && left > 0 && (ok = free_slot(early)); c += ROWB, --left) {
+                    copy_weights(q, early, c, w, lane);
+                    early.next();
+                }
+            }
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(h_bar(), 0, abort_flag(), p.err));
+            int done = p.nst - left;                            // stages whose weights are under way
+            for (int u = begin; u < end && ok; ++u) {
+                const Source q = down_source(u, groups, w, lane);
+                for (int c = 0; c < q.bytes; c += ROWB) {
+                    if (done > 0) {
+                        --done;
+                    } else {
+                        if (!(ok = free_slot(ring))) break;
+                        copy_weights(q, ring, c, w, lane);
+                    }
+                    copy_acts(q, ring, c, w, lane);
+                    async_arrive(ring.full());
+                    ring.next();
+                }
             }
         }
-        if (!ok) {                                              // given up: let the copies in flight land first
-            const int n = (int)(issued < p.nst ? issued : p.nst);
-            for (int i = 0; i < n; ++i) {
-                const long long s = issued - 1 - i;
-                mbar_wait(smem_u32(sm + L.bars) + (uint32_t)(s % p.nst) * 8, (uint32_t)(s / p.nst) & 1u, abort_flag(), p.err,
-                          false);
-            }
-        }
+        async_wait_all();                                       // also when a wait gave up
     }
 
     // ------------------------------------------------------------------------------ router warps
-    __device__ void rank() {
-        const int tid = threadIdx.x - CONS - 32, warp = tid >> 5, lane = tid & 31;
-        const int slots = p.T * p.k;
-        if (warp == 0) {                                        // this block's scores are written: tell, and wait for all
-            named_sync(2, CONS + 32);
-            if (lane == 0) {
-                __threadfence();
-                const unsigned long long t = round_end(atomicAdd(p.bar, 1ull), G);
-                at<volatile int>(L.misc)[2] = grid_wait(p.bar, t, abort_flag(), p.err) ? 1 : 0;
+    // Picks of all tokens (and the experts' masks), or their gates.
+    template <int W, int NPL>
+    __device__ __forceinline__ void rank_tokens(int warp, int lane, bool gates) {
+        constexpr int GROUPS = ROUTE_WARPS * 32 / W;
+        const int l = lane % W;
+        for (int t0 = 0; t0 < p.T; t0 += GROUPS) {
+            const int mine = t0 + warp * (32 / W) + lane / W, t = mine < p.T ? mine : 0;
+            // groups without a token of their own repeat the first, into rows behind the last
+            const int row = mine < p.T ? mine : p.T + warp * (32 / W) + lane / W;
+            int32_t* idx = at<int32_t>(L.pidx) + row * p.k;
+            float* gate = at<float>(L.pgate) + row * p.k;
+            if (gates) {
+                few_gate<W, NPL>(p.logits + (size_t)t * p.E, p.E, p.k, p.mode, p.rbias, l, idx, gate);
+                continue;
             }
+            few_pick<W, NPL>(p.logits + (size_t)t * p.E, p.E, p.k, p.mode, p.rbias, l, idx, gate);
+            for (int j = l; j < p.k && mine < p.T; j += W) {
+                if ((unsigned)idx[j] < (unsigned)p.E) atomicOr(at<uint32_t>(L.mask) + idx[j], 1u << t);
+                else if (blockIdx.x == 0) flag_error(p.err, ERR_EXPERT_RANGE);
+            }
+            __syncwarp();
         }
-        named_sync(3, ROUTE_WARPS * 32);
-        const bool ok = at<volatile int>(L.misc)[2] != 0;
-        int32_t* pidx = at<int32_t>(L.pidx);
-        float* pgate = at<float>(L.pgate);
+    }
+    // few tokens: a warp each; many: 8 or 16 lanes each
+    __device__ __forceinline__ void rank_tokens(int warp, int lane, bool gates) {
+        if (p.T <= ROUTE_WARPS || p.E > 512) {
+            if (p.E <= 64) rank_tokens<32, 2>(warp, lane, gates);
+            else if (p.E <= 256) rank_tokens<32, 8>(warp, lane, gates);
+            else rank_tokens<32, 32>(warp, lane, gates);
+        } else if (p.E <= 64) {
+            rank_tokens<8, 8>(warp, lane, gates);
+        } else if (p.E <= 256) {
+            rank_tokens<16, 16>(warp, lane, gates);
+        } else {
+            rank_tokens<16, 32>(warp, lane, gates);
+        }
+    }
+
+    __device__ void rank() {
+        const int tid = threadIdx.x - CONS - PRODUCERS * 32, warp = tid >> 5, lane = tid & 31;
+        const int slots = p.T * p.k;
+        const int32_t* pidx = at<int32_t>(L.pidx);
+        const float* pgate = at<float>(L.pgate);
         uint32_t* mask = at<uint32_t>(L.mask);
         int* base = at<int>(L.base);
         for (int e = tid; e < p.E; e += ROUTE_WARPS * 32) mask[e] = 0u;
-        float* z = at<float>(L.zl) + warp * p.E;
-        for (int t = warp; t < p.T && ok; t += ROUTE_WARPS) {
-            for (int e = lane; e < p.E; e += 32) z[e] = __ldcg(p.logits + (size_t)t * p.E + e);
-            __syncwarp();
-            warp_route(z, p.E, p.k, p.mode, p.rbias, lane, pidx + t * p.k, pgate + t * p.k);
-            __syncwarp();
-        }
+        if (tid == 0) at<volatile int>(L.misc)[2] = grid_wait(p.bar, at<unsigned long long>(L.turns)[0], abort_flag(), p.err);
         named_sync(3, ROUTE_WARPS * 32);
-        for (int s = tid; s < slots && ok; s += ROUTE_WARPS * 32) {
-            if ((unsigned)pidx[s] < (unsigned)p.E) atomicOr(mask + pidx[s], 1u << (s / p.k));
-            else if (blockIdx.x == 0) flag_error(p.err, ERR_EXPERT_RANGE);
-        }
+        const bool ok = at<volatile int>(L.misc)[2] != 0;
+        if (ok) rank_tokens(warp, lane, false);
         named_sync(3, ROUTE_WARPS * 32);
         if (warp == 0) {                                        // experts met, in ascending order
-            int groups = 0, rows = 0;
-            for (int e0 = 0; e0 < p.E && ok; e0 += 32) {
-                const uint32_t m = e0 + lane < p.E ? mask[e0 + lane] : 0u;
-                const int n = __popc(m);
-                int before = n;
+            const int per = ceil_div(p.E, 32), e0 = lane * per, e1 = e0 + per < p.E ? e0 + per : p.E;
+            int mine = 0;                                       // experts met << 16 | rows: at most 512 of either
+            for (int e = e0; e < e1 && ok; ++e) {
+                const int n = __popc(mask[e]);
+                mine += n + (n > 0 ? 1 << 16 : 0);
+            }
+            int before = mine;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int v = __shfl_up_sync(0xffffffffu, before, o);
-                    if (lane >= o) before += v;
-                }
-                const int all = __shfl_sync(0xffffffffu, before, 31);
-                const uint32_t met = __ballot_sync(0xffffffffu, n > 0);
-                if (n > 0) {
-                    const int gi = groups + __popc(met & ((1u << lane) - 1u));
-                    at<int>(L.ge)[gi] = e0 + lane;
-                    at<uint32_t>(L.gm)[gi] = m;
-                    at<int>(L.gb)[gi] = rows + before - n;
-                    base[e0 + lane] = rows + before - n;
-                }
-                groups += __popc(met);
-                rows += all;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, before, o);
+                if (lane >= o) before += v;
+            }
+            const int groups = __shfl_sync(0xffffffffu, before, 31) >> 16;
+            before -= mine;
+            int gi = before >> 16, rows = before & 0xFFFF;
+            for (int e = e0; e < e1 && ok; ++e) {
+                const uint32_t m = mask[e];
+                if (m == 0u) continue;
+                at<int>(L.ge)[gi] = e;
+                at<uint32_t>(L.gm)[gi] = m;
+                at<int>(L.gb)[gi++] = rows;
+                base[e] = rows;
+                rows += __popc(m);
             }
             if (lane == 0) at<volatile int>(L.misc)[1] = groups;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(route_bar());
         }
+        if (ok) rank_tokens(warp, lane, true);
         named_sync(3, ROUTE_WARPS * 32);
         for (int s = tid; s < slots && ok; s += ROUTE_WARPS * 32) {
             const int e = pidx[s], t = s / p.k;
             if ((unsigned)e < (unsigned)p.E) at<float>(L.gates)[base[e] + __popc(mask[e] & ((1u << t) - 1u))] = pgate[s];
         }
+        named_sync(3, ROUTE_WARPS * 32);
+        if (tid == 0) mbar_arrive(gate_bar());
         if (blockIdx.x == 0 && ok) {
             for (int s = tid; s < slots; s += ROUTE_WARPS * 32) {
                 if (p.idx) p.idx[s] = pidx[s];
@@ -542,53 +788,63 @@ struct Kernel {
             if (p.counts)
                 for (int e = tid; e < p.E; e += ROUTE_WARPS * 32) p.counts[e] = __popc(mask[e]);
         }
-        named_sync(3, ROUTE_WARPS * 32);
-        if (tid == 0) mbar_arrive(route_bar());
     }
 
     // ------------------------------------------------------------------------------ consumers
-    // Router scores of this block's experts (rows blockIdx.x, + G, ...) for all tokens.
-    __device__ void scores(float* red, const Me& me) {
+    // Router scores.  A task is one expert with TB tokens; 1, 2, 4 or 8 warps split its columns, as many as the
+    // grid has warps for, so that with few experts and tokens a warp's loads are all under way at once.
+    template <int TB>
+    __device__ __forceinline__ void scores(float* red, const Me& me) {
         constexpr int VEC = FR == W_F32 ? 4 : 8;
-        const int nv = p.d / VEC, tid = threadIdx.x;
-        const uint4* x = static_cast<const uint4*>(p.x);
-        const uint4* cen = static_cast<const uint4*>(p.cen);
-        for (int e = blockIdx.x; e < p.E; e += G) {
-            float acc[NT * 8];
+        const int tbs = ceil_div(p.T, TB), tasks = p.E * tbs;
+        int S = CONS_WARPS;
+        while (S > 1 && (long long)tasks * S > (long long)G * CONS_WARPS) S >>= 1;
+        const int per = CONS_WARPS / S, part = me.warp & (S - 1), sub = me.warp / S;
+        const int nv = p.d / VEC, n = ceil_div(ceil_div(nv, 32), S) * 32;    // vectors of a warp
+        const int v1 = (part + 1) * n < nv ? (part + 1) * n : nv;
+        for (int t0 = blockIdx.x * per; t0 < tasks; t0 += G * per) {
+            const int task = t0 + sub, e = task % p.E, tok = task / p.E * TB;
+            float acc[TB] = {};
+            if (task < tasks) {
+                const uint4* c = static_cast<const uint4*>(p.cen) + (size_t)e * nv;
+                const uint4* x[TB];
 #pragma unroll
-            for (int t = 0; t < NT * 8; ++t) acc[t] = 0.f;
-            for (int i = tid; i < nv; i += CONS) {
-                const uint4 c = __ldg(cen + (size_t)e * nv + i);
-                const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+                for (int t = 0; t < TB; ++t)                    // tokens that are not there repeat the last one
+                    x[t] = static_cast<const uint4*>(p.x) + (size_t)(tok + t < p.T ? tok + t : p.T - 1) * nv;
+#pragma unroll 4
+                for (int i = part * n + me.lane; i < v1; i += 32) {
+                    const uint4 w = __ldg(c + i);
+                    const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int t = 0; t < NT * 8; ++t) {
-                    if (t >= p.T) break;
-                    const uint4 v = __ldg(x + (size_t)t * nv + i);
-                    const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+                    for (int t = 0; t < TB; ++t) {
+                        const uint4 v = __ldg(x[t] + i);
+                        const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        if (FR == W_F32) {
-                            acc[t] = fmaf(__uint_as_float(vw[q]), __uint_as_float(cw[q]), acc[t]);
-                        } else {
-                            acc[t] = fmaf(__uint_as_float(vw[q] << 16), __uint_as_float(cw[q] << 16), acc[t]);
-                            acc[t] = fmaf(__uint_as_float(vw[q] & 0xFFFF0000u), __uint_as_float(cw[q] & 0xFFFF0000u), acc[t]);
+                        for (int q = 0; q < 4; ++q) {
+                            if (FR == W_F32) {
+                                acc[t] = fmaf(__uint_as_float(vw[q]), __uint_as_float(cw[q]), acc[t]);
+                            } else {
+                                acc[t] = fmaf(__uint_as_float(vw[q] << 16), __uint_as_float(cw[q] << 16), acc[t]);
+                                acc[t] = fmaf(__uint_as_float(vw[q] & 0xFFFF0000u), __uint_as_float(cw[q] & 0xFFFF0000u), acc[t]);
+                            }
                         }
                     }
                 }
             }
 #pragma unroll
-            for (int t = 0; t < NT * 8; ++t) {
-                if (t >= p.T) break;
+            for (int t = 0; t < TB; ++t) {
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) acc[t] += __shfl_xor_sync(0xffffffffu, acc[t], o);
-                if (me.lane == 0) red[me.warp * NT * 8 + t] = acc[t];
+                if (me.lane == t) red[me.warp * TB + t] = acc[t];
             }
             named_sync(1, CONS);
-            if (tid < p.T) {
-                float z = red[tid];
-#pragma unroll
-                for (int w = 1; w < CONS_WARPS; ++w) z += red[w * NT * 8 + tid];
-                p.logits[(size_t)tid * p.E + e] = z;
+            if ((int)threadIdx.x < per * TB) {
+                const int q = threadIdx.x / TB, t = threadIdx.x % TB, mine = t0 + q;
+                if (mine < tasks && mine / p.E * TB + t < p.T) {
+                    float z = 0.f;
+                    for (int w = 0; w < S; ++w) z += red[(q * S + w) * TB + t];
+                    p.logits[(size_t)(mine / p.E * TB + t) * p.E + mine % p.E] = z;
+                }
             }
             named_sync(1, CONS);
         }
@@ -599,55 +855,54 @@ struct Kernel {
         return q.shared ? 1.f : at<float>(L.gates)[q.row + __popc(q.mask & ((1u << tok) - 1u))];
     }
 
+    // The fragment of a unit that this warp finishes, or -1: they go round the warps.
+    __device__ __forceinline__ int my_frag(const Me& me, int turn) const {
+        const int f = (me.warp - turn * FRAGS) & (CONS_WARPS - 1);
+        return f < FRAGS ? f : -1;
+    }
+
     template <int F>
-    __device__ __forceinline__ void up(Me& me, const Group& q, int r0, float4* red) {
-        const int g = me.lane >> 2;
+    __device__ __forceinline__ void up(Me& me, const Group& q, float4* red) {
         if constexpr (F == W_F32) {
-            const float* ptr[NT * 8];
             float acc[NT * 8];
 #pragma unroll
-            for (int n = 0; n < NT * 8; ++n) {
-                ptr[n] = (q.mask >> n) & 1u ? static_cast<const float*>(p.x) + (size_t)n * p.d : nullptr;
-                acc[n] = 0.f;
-            }
-            unit_f32<NT>(acc, me, ptr, p.d);
+            for (int n = 0; n < NT * 8; ++n) acc[n] = 0.f;
+            unit_f32<NT>(acc, me, p.d, q.mask);
             put_f32<NT>(red, acc, me);
         } else {
-            const __nv_bfloat16* ptr[NT];
-            float acc[NT * 4];
+            float acc[R][NT * 4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int n = nt * 8 + g;
-                ptr[nt] = (q.mask >> n) & 1u ? static_cast<const __nv_bfloat16*>(p.x) + (size_t)n * p.d : nullptr;
-            }
+            for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int i = 0; i < NT * 4; ++i) acc[i] = 0.f;
-            const uint8_t* sfw[2] = {nullptr, nullptr};
-            if (F == W_MX) {                                    // w1's half of the tile, and w3's
-                const int r = r0 + g;
-                sfw[0] = p.R.sf13 + ((size_t)q.e * ceil_div(p.I, 128) + r / 128) * ceil_div(p.d, 128) * 1024 + (r & 31) * 16 +
-                         ((r >> 5) & 3) * 4;
-                sfw[1] = sfw[0] + 512;
-            }
-            unit_mma<F, NT, 1>(acc, me, ptr, 0, p.d, q.mask, sfw);
-            put_frag<NT>(red, acc, me);
+                for (int j = 0; j < NT * 4; ++j) acc[i][j] = 0.f;
+            unit_mma<FR, F, NT, 1, R>(acc, me, Stage<FR, R>::scales(p.T), p.d, q.mask);
+            put_frag<NT, R>(red, acc, me);
         }
     }
 
-    // h of one unit from the summed fragments (token group nt).
-    __device__ __forceinline__ void finish_up(const Group& q, int r0, float4 c, int nt, int lane) {
-        const int I = q.shared ? p.Is : p.I, r = r0 + (lane >> 2);
-        if (r >= I) return;
+    // Scales and biases of a unit's fragment, for the lane's row of w1 and of w3: loaded before the unit.
+    struct Fin {
+        float s1, s3, b1, b3;
+    };
+    __device__ __forceinline__ Fin fin_of(const Group& q, int r) const {
+        Fin f = {1.f, 1.f, 0.f, 0.f};
+        const int I = q.shared ? p.Is : p.I;
+        if (r >= I) return f;
         const FfnWeights& W = q.shared ? p.Sh : p.R;
         const size_t at_row = (size_t)q.e * I + r;
-        float s1 = 1.f, s3 = 1.f;
-        if (FR == W_E4M3 && !q.shared) { s1 = W.s1[at_row]; s3 = W.s3[at_row]; }
-        const float b1 = p.bias ? bias_at(W.b1, at_row) : 0.f, b3 = p.bias ? bias_at(W.b3, at_row) : 0.f;
+        if (FR == W_E4M3 && !q.shared) { f.s1 = W.s1[at_row]; f.s3 = W.s3[at_row]; }
+        if (p.bias) { f.b1 = bias_at(W.b1, at_row); f.b3 = bias_at(W.b3, at_row); }
+        return f;
+    }
+
+    // h of one unit's row r from the summed fragment (token group nt).
+    __device__ __forceinline__ void finish_up(const Group& q, int r, const Fin& f, float4 c, int nt, int lane) {
+        if (r >= (q.shared ? p.Is : p.I)) return;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int tok = nt * 8 + (lane & 3) * 2 + i;
             if (!((q.mask >> tok) & 1u)) continue;
-            const float a = (i ? c.y : c.x) * s1 + b1, b = (i ? c.w : c.z) * s3 + b3;
+            const float a = (i ? c.y : c.x) * f.s1 + f.b1, b = (i ? c.w : c.z) * f.s3 + f.b3;
             const float h = silu_f32(a) * b * gate_of(q, tok);
             const size_t row = q.row + __popc(q.mask & ((1u << tok) - 1u));
             if (FR == W_F32) {
@@ -662,92 +917,112 @@ struct Kernel {
         }
     }
 
-    template <int F>
-    __device__ __forceinline__ void down(float (&acc)[FR == W_F32 ? NT * 8 : NT * 4], Me& me, const Group& q, int cb) {
-        const int g = me.lane >> 2, K = q.shared ? p.Is : p.I;
-        if constexpr (F == W_F32) {
-            const float* ptr[NT * 8];
+    using Acc = float[R][FR == W_F32 ? NT * 8 : NT * 4];
+
+    // acc (put_frag's order, fp32: put_f32's) += gate * b2 of the group's expert, for the rows b2_of has loaded.
+    struct B2 {
+        float b[R][2];
+    };
+    __device__ __forceinline__ B2 b2_of(const Me& me, const Group& q, int cb) const {
+        const void* b2 = q.shared ? p.Sh.b2 : p.R.b2;
+        B2 o;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = cb * DOWN + (FR == W_F32 ? me.lane >> 1 : i * 16 + h * 8 + (me.lane >> 2));
+                o.b[i][h] = r < p.d ? bias_at(b2, (size_t)q.e * p.d + r) : 0.f;
+            }
+        return o;
+    }
+    __device__ __forceinline__ void add_b2(Acc& acc, const Me& me, const Group& q, const B2& b) const {
+        if constexpr (FR == W_F32) {
+            if (me.lane & 1) return;
 #pragma unroll
             for (int n = 0; n < NT * 8; ++n)
-                ptr[n] = (q.mask >> n) & 1u
-                             ? static_cast<const float*>(p.h) + (size_t)(q.row + __popc(q.mask & ((1u << n) - 1u))) * p.Hs
-                             : nullptr;
-            unit_f32<NT>(acc, me, ptr, K);
+                if ((q.mask >> n) & 1u) acc[0][n] = fmaf(gate_of(q, n), b.b[0][0], acc[0][n]);
         } else {
-            const __nv_bfloat16* ptr[NT];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int n = nt * 8 + g;
-                ptr[nt] = (q.mask >> n) & 1u ? static_cast<const __nv_bfloat16*>(p.h) +
-                                                   (size_t)(q.row + __popc(q.mask & ((1u << n) - 1u))) * 2 * p.Hs
-                                             : nullptr;
-            }
-            const uint8_t* sfw[2] = {nullptr, nullptr};
-            if (F == W_MX) {
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int r = cb * ROWS + g + 8 * i;
-                    sfw[i] = p.R.sf2 + ((size_t)q.e * ceil_div(p.d, 256) + r / 256) * ceil_div(p.I, 128) * 1024 +
-                             ((r >> 7) & 1) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4;
+                for (int j = 0; j < 2; ++j) {
+                    const int tok = nt * 8 + (me.lane & 3) * 2 + j;
+                    if (!((q.mask >> tok) & 1u)) continue;
+                    const float gate = gate_of(q, tok);
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) acc[i][nt * 4 + h * 2 + j] = fmaf(gate, b.b[i][h], acc[i][nt * 4 + h * 2 + j]);
                 }
-            }
-            if (F == W_E4M3) {                                  // per-row scales differ from expert to expert
-                float t[NT * 4];
-#pragma unroll
-                for (int i = 0; i < NT * 4; ++i) t[i] = 0.f;
-                unit_mma<F, NT, 2>(t, me, ptr, p.Hs, K, q.mask, sfw);
-                const int r = cb * ROWS + g;
-                const float* s2 = p.R.s2 + (size_t)q.e * p.d;
-                const float f0 = r < p.d ? s2[r] : 0.f, f1 = r + 8 < p.d ? s2[r + 8] : 0.f;
-#pragma unroll
-                for (int i = 0; i < NT * 4; ++i) acc[i] = fmaf(t[i], (i & 2) ? f1 : f0, acc[i]);
-            } else {
-                unit_mma<F, NT, 2>(acc, me, ptr, p.Hs, K, q.mask, sfw);
-            }
         }
     }
 
-    // A column block's sums over the block's groups [u0, u1) of `groups`: to the output when they are all,
-    // else to the partial sums; the block that completes the count adds those of all blocks in order.
-    __device__ __forceinline__ void finish_down(float4 c, int cb, int u0, int u1, int groups, long long U, int nt, int lane) {
+    template <int F>
+    __device__ __forceinline__ void down(Acc& acc, Me& me, const Group& q, int cb) {
+        const int K = q.shared ? p.Is : p.I;
+        const bool b2 = p.bias && me.warp == q.row % CONS_WARPS;    // one warp's: loaded before the unit, added after it
+        B2 b;
+        if (b2) b = b2_of(me, q, cb);
+        if constexpr (F == W_F32) {
+            unit_f32<NT>(acc[0], me, K, q.mask);
+        } else {
+            if (F == W_E4M3) {                                  // per-row scales differ from expert to expert
+                float t[R][NT * 4], f[R][2];
+                const float* s2 = p.R.s2 + (size_t)q.e * p.d;
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+#pragma unroll
+                    for (int j = 0; j < NT * 4; ++j) t[i][j] = 0.f;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = cb * DOWN + i * 16 + h * 8 + (me.lane >> 2);
+                        f[i][h] = r < p.d ? s2[r] : 0.f;
+                    }
+                }
+                unit_mma<FR, F, NT, 2, R>(t, me, 0, K, q.mask);
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int j = 0; j < NT * 4; ++j) acc[i][j] = fmaf(t[i][j], f[i][(j >> 1) & 1], acc[i][j]);
+            } else {
+                unit_mma<FR, F, NT, 2, R>(acc, me, Stage<FR, R>::scales(p.T), K, q.mask);
+            }
+        }
+        if (b2) add_b2(acc, me, q, b);
+    }
+
+    // A column block's sums of fragment f over the block's groups [u0, u1) of `groups`: to the output when they
+    // are all, else to the partial sums; the block that completes the count adds those of all blocks in order.
+    __device__ __forceinline__ void finish_down(float4 c, int cb, int u0, int u1, int groups, uint32_t U, int f, int lane) {
         if (u1 - u0 != groups) {
-            const int me = blockIdx.x;
-            auto slot = [&](int b) { return p.part + (((size_t)b * 2 + (down_start(U, b) / groups == cb ? 0 : 1)) * NT + nt) * 32 + lane; };
-            __stcg(slot(me), c);
+            const int first = cb * groups;                      // a block's first partial column block, or its last
+            auto slot = [&](int b, bool starts) { return p.part + (((size_t)b * 2 + (starts ? 0 : 1)) * FRAGS + f) * 32 + lane; };
+            __stcg(slot(blockIdx.x, down_start(U, blockIdx.x) >= first), c);
             __threadfence();
             __syncwarp();
             unsigned old = 0;
-            if (lane == 0) old = atomicAdd(p.cnt + cb * NT + nt, (unsigned)(u1 - u0));
+            if (lane == 0) old = atomicAdd(p.cnt + cb * FRAGS + f, (unsigned)(u1 - u0));
             old = __shfl_sync(0xffffffffu, old, 0);
             if (old + (unsigned)(u1 - u0) != (unsigned)groups) return;
             __threadfence();
-            const int first = cb * groups, last = first + groups;   // units of the column block (U < 2^31)
-            int b = me;
-            while (b > 0 && down_start(U, b) > first) --b;
             c = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (; b < G && down_start(U, b) < last; ++b) {
-                if (down_start(U, b + 1) == down_start(U, b)) continue;
-                const float4 v = __ldcg(slot(b));
+            const int b1 = down_block(U, first + groups - 1);
+            for (int b = down_block(U, first); b <= b1; ++b) {
+                const int at = down_start(U, b);
+                if (down_start(U, b + 1) == at) continue;
+                const float4 v = __ldcg(slot(b, at >= first));
                 c.x += v.x; c.y += v.y; c.z += v.z; c.w += v.w;
             }
         }
+        const int nt = f % NT;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = cb * ROWS + (lane >> 2) + 8 * i;
+        for (int h = 0; h < 2; ++h) {
+            const int r = cb * DOWN + f / NT * 16 + (lane >> 2) + 8 * h;
             if (r >= p.d) continue;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int tok = nt * 8 + (lane & 3) * 2 + j;
-                if (tok >= p.T) continue;
-                float v = i ? (j ? c.w : c.z) : (j ? c.y : c.x);
-                if (p.bias) {
-                    for (int s = 0; s < p.Ks; ++s) v += bias_at(p.Sh.b2, (size_t)s * p.d + r);
-                    for (int s = 0; s < p.k; ++s) {
-                        const int e = at<int32_t>(L.pidx)[tok * p.k + s];
-                        if ((unsigned)e < (unsigned)p.E) v = fmaf(at<float>(L.pgate)[tok * p.k + s], bias_at(p.R.b2, (size_t)e * p.d + r), v);
-                    }
-                }
-                static_cast<T*>(p.out)[(size_t)tok * p.d + r] = from_f32<T>(v);
+                if (tok < p.T) static_cast<T*>(p.out)[(size_t)tok * p.d + r] = from_f32<T>(h ? (j ? c.w : c.z) : (j ? c.y : c.x));
             }
         }
     }
@@ -755,13 +1030,15 @@ struct Kernel {
     __device__ void consume() {
         Me me = {ring(), (int)(threadIdx.x >> 5), (int)(threadIdx.x & 31), abort_flag(), p.err};
         float4* red0 = at<float4>(L.red);
-        const int cbs = ceil_div(p.d, ROWS);
-        for (int i = blockIdx.x * CONS + threadIdx.x; i < cbs * NT; i += G * CONS) p.cnt[i] = 0u;
-        scores(reinterpret_cast<float*>(red0), me);
-        named_arrive(2, CONS + 32);
+        const int cbs = ceil_div(p.d, DOWN);
+        for (int i = blockIdx.x * CONS + threadIdx.x; i < cbs * FRAGS; i += G * CONS) p.cnt[i] = 0u;
+        if (p.T == 1) scores<1>(reinterpret_cast<float*>(red0), me);
+        else scores<4>(reinterpret_cast<float*>(red0), me);
+        named_sync(1, CONS);                                    // the block's scores are written
+        if (threadIdx.x == 0) grid_arrive(p.bar);
 
         int turn = 0;
-        auto buffer = [&] { return red0 + (turn & 1) * CONS_WARPS * NT * 32; };
+        auto buffer = [&] { return red0 + (turn & 1) * CONS_WARPS * FRAGS * 32; };
         const int su = shared_units();
         int units = su, met = 0;
         bool routed = false;
@@ -772,25 +1049,26 @@ struct Kernel {
                 named_sync(1, CONS);
                 met = at<volatile int>(L.misc)[3];
                 routed = true;
-                units = su + met * ceil_div(p.I, 8);
+                units = su + met * ceil_div(p.I, UP);
             }
             if (u >= units) break;
             Group q;
             int r0;
             up_unit(u, q, r0);
-            if (FR != FS && !q.shared) up<FR>(me, q, r0, buffer());
-            else up<FS>(me, q, r0, buffer());
+            const int f = my_frag(me, turn), r = r0 + f / NT * 8 + (me.lane >> 2);
+            Fin fin = {};
+            if (f >= 0) fin = fin_of(q, r);
+            if (FR != FS && !q.shared) up<FR>(me, q, buffer());
+            else up<FS>(me, q, buffer());
             named_sync(1, CONS);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                if ((turn * NT + nt) % CONS_WARPS == me.warp) finish_up(q, r0, take_frag<NT>(buffer(), nt, me.lane), nt, me.lane);
+            if (f >= 0 && !q.shared) mbar_wait(gate_bar(), 0, abort_flag(), p.err);
+            if (f >= 0) finish_up(q, r, fin, take_frag<FRAGS>(buffer(), f, me.lane), f % NT, me.lane);
             ++turn;
         }
         named_sync(1, CONS);                                    // the block's h is written
         if (threadIdx.x == 0) {
-            __threadfence();
-            const unsigned long long t = round_end(atomicAdd(p.bar + 1, 1ull), G);
-            grid_wait(p.bar + 1, t, abort_flag(), p.err);
+            grid_arrive(p.bar + 1);
+            if (grid_wait(p.bar + 1, at<unsigned long long>(L.turns)[1], abort_flag(), p.err)) mbar_arrive(h_bar());
         }
         named_sync(1, CONS);
 
@@ -800,41 +1078,45 @@ struct Kernel {
                 static_cast<T*>(p.out)[i] = from_f32<T>(0.f);
             return;
         }
-        const long long U = (long long)cbs * groups;
+        const uint32_t U = (uint32_t)(cbs * groups);
         const int end = down_start(U, blockIdx.x + 1);
         for (int u = down_start(U, blockIdx.x); u < end;) {
             const int cb = u / groups, u0 = u, u1 = (cb + 1) * groups < end ? (cb + 1) * groups : end;
-            float acc[FR == W_F32 ? NT * 8 : NT * 4];
+            Acc acc;
 #pragma unroll
-            for (float& a : acc) a = 0.f;
+            for (auto& row : acc)
+#pragma unroll
+                for (float& a : row) a = 0.f;
             for (; u < u1; ++u) {
                 const Group q = group(u % groups);
                 if (FR != FS && !q.shared) down<FR>(acc, me, q, cb);
                 else down<FS>(acc, me, q, cb);
             }
-            if constexpr (FR == W_F32) put_f32<NT>(buffer(), acc, me);
-            else put_frag<NT>(buffer(), acc, me);
+            if constexpr (FR == W_F32) put_f32<NT>(buffer(), acc[0], me);
+            else put_frag<NT, R>(buffer(), acc, me);
             named_sync(1, CONS);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-                if ((turn * NT + nt) % CONS_WARPS == me.warp)
-                    finish_down(take_frag<NT>(buffer(), nt, me.lane), cb, u0, u1, groups, U, nt, me.lane);
+            const int f = my_frag(me, turn);
+            if (f >= 0) finish_down(take_frag<FRAGS>(buffer(), f, me.lane), cb, u0, u1, groups, U, f, me.lane);
             ++turn;
         }
     }
 };
 
-template <int FR, int NT>
+template <int FR, int NT, int R>
 __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) char sm[];
-    Kernel<FR, NT> k(p, sm);
+    Kernel<FR, NT, R> k(p, sm);
     if (threadIdx.x == 0) {
         const uint32_t bars = smem_u32(sm + k.L.bars);
         for (int s = 0; s < p.nst; ++s) {
-            mbar_init(bars + s * 8, 1);
+            mbar_init(bars + s * 8, PRODUCERS * 32);            // every producer thread's copies
             mbar_init(bars + (MAX_STAGES + s) * 8, CONS_WARPS);
         }
         mbar_init(k.route_bar(), 1);
+        mbar_init(k.h_bar(), 1);
+        mbar_init(k.gate_bar(), 1);
+        // this block has not arrived yet, so that the barriers' rounds cannot end before it has read them
+        for (int i = 0; i < 2; ++i) k.template at<unsigned long long>(k.L.turns)[i] = round_end(load_acquire(p.bar + i), gridDim.x);
         int* misc = k.template at<int>(k.L.misc);
         misc[0] = misc[1] = misc[2] = misc[3] = 0;              // given up; experts met; scores complete; the consumers' view
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -842,12 +1124,12 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
     __syncthreads();
     const int warp = threadIdx.x >> 5;
     if (warp < CONS_WARPS) k.consume();
-    else if (warp == PRODUCER) k.produce();
+    else if (warp < CONS_WARPS + PRODUCERS) k.produce(warp - CONS_WARPS);
     else k.rank();
 }
 
 size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
-constexpr int GRID_MAX = 256;
+constexpr int GRID_MAX = 256, MAX_FRAGS = 4;
 
 struct Layout {
     size_t logits, h, part, cnt, total;
@@ -861,29 +1143,38 @@ Layout few_layout(const Dims& D) {
     size_t o = 256;
     L.logits = o; o += al256(T * D.E * 4);
     L.h = o; o += al256(T * (D.k + D.Ks) * L.Hs * 4);           // two bf16 parts, or fp32
-    L.part = o; o += al256((size_t)GRID_MAX * 2 * 2 * 32 * 16);
-    L.cnt = o; o += al256((size_t)ceil_div(D.d, ROWS) * 2 * 4);
+    L.part = o; o += al256((size_t)GRID_MAX * 2 * MAX_FRAGS * 32 * 16);
+    L.cnt = o; o += al256((size_t)ceil_div(D.d, 16) * MAX_FRAGS * 4);
     L.total = o;
     return L;
 }
 
-template <int FR, int NT>
-cudaError_t launch(Params& p, cudaStream_t st) {
-    const Smem none(0, NT, p.T, p.E, p.k);
-    int n = (SMEM_LIMIT - none.total) / STAGE_BYTES;
-    p.nst = n > MAX_STAGES ? MAX_STAGES : n;
-    const Smem L(p.nst, NT, p.T, p.E, p.k);
-    auto kern = few_kernel<FR, NT>;
+template <int FR, int NT, int R>
+cudaError_t launch(Params& p, int grid, cudaStream_t st) {
+    const int rest = Smem(0, R * NT, p.T, p.E, p.k).total, rows = 16 * R * Fmt<FR, FR>::ROWB;
+    p.stage = Stage<FR, R>::bytes(p.T);
+    int n = (SMEM_LIMIT - rest) / p.stage;
+    n = n > MAX_STAGES ? MAX_STAGES : n;
+    p.nst = n * rows > RING_BYTES ? RING_BYTES / rows : n;
+    const Smem L(p.nst * p.stage, R * NT, p.T, p.E, p.k);
+    auto kern = few_kernel<FR, NT, R>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
     if (e != cudaSuccess) return e;
-    const int grid = num_sms() < GRID_MAX ? num_sms() : GRID_MAX;
     void* args[] = {&p};
     return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(grid), dim3(THREADS), args, L.total, st);
 }
 
+// Two row tiles use every activation fragment twice; one leaves twice as many units to spread.
 template <int FR>
 cudaError_t launch_t(Params& p, cudaStream_t st) {
-    return p.T <= 8 ? launch<FR, 1>(p, st) : launch<FR, 2>(p, st);
+    const int grid = num_sms() < GRID_MAX ? num_sms() : GRID_MAX;
+    if constexpr (FR == W_F32) {
+        return p.T <= 8 ? launch<FR, 1, 1>(p, grid, st) : launch<FR, 2, 1>(p, grid, st);
+    } else {
+        const bool tall = p.k * ceil_div(p.I, 16) + p.Ks * ceil_div(p.Is, 16) >= 4 * grid;
+        if (p.T <= 8) return tall ? launch<FR, 1, 2>(p, grid, st) : launch<FR, 1, 1>(p, grid, st);
+        return tall ? launch<FR, 2, 2>(p, grid, st) : launch<FR, 2, 1>(p, grid, st);
+    }
 }
 
 }  // namespace
