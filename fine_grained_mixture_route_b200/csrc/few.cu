@@ -25,17 +25,23 @@
 // Products: mma.sync m16n8k16 with the weights as the 16-row operand and the tokens as the 8 columns, fp32
 // accumulators.  tcgen05's smallest tile is 64 or 128 weight rows, too coarse to spread a few experts evenly
 // over 148 SMs, and takes 8-bit weights only against 8-bit activations; here the bound is HBM, the tensor
-// pipe idles.  8-bit codes become bf16 exactly; scales are applied to fp32 sums (block scales: each run of
-// 32 has its own sum).  Activations are not quantised: x is bf16 as given, and h is kept as the sum of two
-// bf16 numbers (16 significant bits).  A thread's k-columns need only be the same for both operands, so
-// every fragment is a plain 16- or 8-byte load, without ldmatrix.
+// pipe idles.  Scales are applied to fp32 sums (block scales: each run of 32 has its own sum).  Activations are
+// not quantised: x is bf16 as given, and h is kept as the sum of two bf16 numbers (16 significant bits).
+// 8-bit codes become fp16, exactly and in one instruction a pair (bf16 takes four, and the conversions then
+// bound the kernel: 196 us instead of XX for the products of w1, w3 of 22 experts of 2048 x 7168).  Their
+// activations are therefore fp16 too, each row times a power of two that brings its largest finite value into
+// [2^14, 2^15): x in one number (its 8 bits are kept down to 2^-28 of that, and 2^-40 of it is the largest error), h in
+// two (22 bits), for which the rows' largest values have to be known: one grid barrier more, behind which the
+// rows are converted, while the first weights of w2 arrive.
+// A thread's k-columns need only be the same for both operands, so every fragment is a plain 16- or 8-byte
+// load, without ldmatrix.
 // fp32 layers take the same route with FFMA.
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "common.cuh"
 #include "launch.h"
 #include "pipe.cuh"
-#include "route.cuh"
 
 namespace moe {
 namespace {
@@ -81,10 +87,13 @@ struct Params {
     int32_t* counts;
     float* logits;                                              // [T][E]
     void* h;                                                    // bf16 [rows][2][Hs] (high, low part), fp32 [rows][Hs]
+    __half* x16;                                                // 8-bit experts: [T][d], row t times 1 / xf[t]
+    float* xf;
+    unsigned* hmax;                                             // their rows' largest finite |h|, as bits
     float4* part;                                               // [blocks][2][R NT][32]
     unsigned* cnt;                                              // [column blocks][R NT]: units already added up
     uint32_t* err;
-    unsigned long long* bar;                                    // two grid barriers (arrivals, ever growing)
+    unsigned long long* bar;                                    // three grid barriers (arrivals, ever growing)
     int T, d, E, I, k, Ks, Is, Hs, mode, nst, stage;
     bool bias;
 };
@@ -99,7 +108,7 @@ struct Smem {
         auto take = [&](int bytes) { const int at = o; o += (bytes + 15) / 16 * 16; return at; };
         ring = take(ring_bytes);
         bars = take((2 * MAX_STAGES + 3) * 8);
-        turns = take(2 * 8);
+        turns = take(3 * 8);
         red = take(2 * CONS_WARPS * frags * 32 * 16);
         mask = take(E * 4);
         base = take(E * 4);
@@ -109,7 +118,7 @@ struct Smem {
         gates = take(T * k * 4);
         pidx = take((T + SPARE) * k * 4);
         pgate = take((T + SPARE) * k * 4);
-        misc = take(16);
+        misc = take(32);
         total = o;
     }
 };
@@ -136,17 +145,25 @@ __device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Four e4m3 codes as two bf16 pairs (exact; NaN stays NaN): the upper halves of the fp32 values, picked by bytes,
-// as conversions that round run at a fraction of the rate.
-__device__ __forceinline__ uint2 bf16_of_codes(uint32_t w) {
-    uint32_t o[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> (16 * i)), __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-        o[i] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
-    }
-    return make_uint2(o[0], o[1]);
+__device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four e4m3 codes as two fp16 pairs (exact; NaN stays NaN).
+__device__ __forceinline__ uint2 f16_of_codes(uint32_t w) {
+    const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w, __NV_E4M3);
+    const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+    return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// The power of two that brings m (finite, >= 0) into [2^14, 2^15), for m below 2^-112 less; its reciprocal is normal.
+__device__ __forceinline__ float f16_scale(float m) {
+    const int e = (int)(__float_as_uint(m) >> 23) - 127;        // subnormal or 0: -127
+    return __uint_as_float((uint32_t)((14 - e > 126 ? 126 : 14 - e) + 127) << 23);
 }
 
 __device__ __forceinline__ float scale_of_byte(uint32_t b) { return __uint_as_float(b ? b << 23 : 0x00400000u); }
@@ -246,8 +263,8 @@ __device__ __forceinline__ void mma_stage(float (&acc)[R][NT * 4], uint32_t stag
                     a1 = lds128(at + 8 * L::PITCH);
                 } else {
                     const uint2 q0 = lds64(at), q1 = lds64(at + 8 * L::PITCH);
-                    const uint2 l0 = bf16_of_codes(q0.x), h0 = bf16_of_codes(q0.y);
-                    const uint2 l1 = bf16_of_codes(q1.x), h1 = bf16_of_codes(q1.y);
+                    const uint2 l0 = f16_of_codes(q0.x), h0 = f16_of_codes(q0.y);
+                    const uint2 l1 = f16_of_codes(q1.x), h1 = f16_of_codes(q1.y);
                     a0 = make_uint4(l0.x, l0.y, h0.x, h0.y);
                     a1 = make_uint4(l1.x, l1.y, h1.x, h1.y);
                 }
@@ -259,8 +276,13 @@ __device__ __forceinline__ void mma_stage(float (&acc)[R][NT * 4], uint32_t stag
                 float* to = F == W_MX ? t : acc[i] + nt * 4;
 #pragma unroll
                 for (int q = 0; q < HL; ++q) {
-                    mma_bf16(to, a0.x, a1.x, a0.y, a1.y, b[nt][q].x, b[nt][q].y);
-                    mma_bf16(to, a0.z, a1.z, a0.w, a1.w, b[nt][q].z, b[nt][q].w);
+                    if (F == W_BF16) {
+                        mma_bf16(to, a0.x, a1.x, a0.y, a1.y, b[nt][q].x, b[nt][q].y);
+                        mma_bf16(to, a0.z, a1.z, a0.w, a1.w, b[nt][q].z, b[nt][q].w);
+                    } else {
+                        mma_f16(to, a0.x, a1.x, a0.y, a1.y, b[nt][q].x, b[nt][q].y);
+                        mma_f16(to, a0.z, a1.z, a0.w, a1.w, b[nt][q].z, b[nt][q].w);
+                    }
                 }
                 if (F == W_MX) {
                     const float f0 = scale_of_byte((sf[i][0] >> (8 * s)) & 0xFFu), f1 = scale_of_byte((sf[i][1] >> (8 * s)) & 0xFFu);
@@ -477,6 +499,7 @@ struct Kernel {
     static_assert(FR != W_F32 || R == 1, "fp32 units have one row tile");
     static constexpr int FRAGS = R * NT, UP = 8 * R, DOWN = 16 * R;    // fragments, rows of w1 (and w3) and of w2 of a unit
     static constexpr int FS = FR == W_F32 ? W_F32 : W_BF16;
+    static constexpr bool Q8 = FR == W_E4M3 || FR == W_MX;
     using T = typename std::conditional<FR == W_F32, float, __nv_bfloat16>::type;
 
     const Params& p;
@@ -489,6 +512,7 @@ struct Kernel {
     __device__ __forceinline__ U* at(int off) const { return reinterpret_cast<U*>(sm + off); }
     __device__ __forceinline__ volatile int* abort_flag() const { return at<int>(L.misc); }
     __device__ __forceinline__ int n_routed() const { return at<volatile int>(L.misc)[1]; }
+    __device__ __forceinline__ int h_rows() const { return at<volatile int>(L.misc)[4]; }    // of picked experts
     __device__ __forceinline__ uint32_t route_bar() const { return smem_u32(sm + L.bars) + 2 * MAX_STAGES * 8; }
     __device__ __forceinline__ uint32_t h_bar() const { return route_bar() + 8; }
     __device__ __forceinline__ uint32_t gate_bar() const { return route_bar() + 16; }
@@ -602,7 +626,7 @@ struct Kernel {
         Source q;
         q.bytes = p.d * esz; q.esz = esz;
         q.rows(static_cast<const char*>(m) + ((size_t)g.e * I + r0) * q.bytes, 8, I - r0, lane);
-        q.act = static_cast<const char*>(p.x) + lane * 16;
+        q.act = (Q8 && !g.shared ? reinterpret_cast<const char*>(p.x16) : static_cast<const char*>(p.x)) + lane * 16;
         q.act_row = p.d * (int)sizeof(T); q.act_low = 0;
         q.mask = g.mask; q.by_token = true; q.sf = nullptr;
         const int r = r0 + (lane >> 4) * 8 + (lane & 7);        // of the lane's row in the stage
@@ -756,7 +780,7 @@ struct Kernel {
                 const int v = __shfl_up_sync(0xffffffffu, before, o);
                 if (lane >= o) before += v;
             }
-            const int groups = __shfl_sync(0xffffffffu, before, 31) >> 16;
+            const int all = __shfl_sync(0xffffffffu, before, 31), groups = all >> 16;
             before -= mine;
             int gi = before >> 16, rows = before & 0xFFFF;
             for (int e = e0; e < e1 && ok; ++e) {
@@ -768,7 +792,10 @@ struct Kernel {
                 base[e] = rows;
                 rows += __popc(m);
             }
-            if (lane == 0) at<volatile int>(L.misc)[1] = groups;
+            if (lane == 0) {
+                at<volatile int>(L.misc)[1] = groups;
+                at<volatile int>(L.misc)[4] = all & 0xFFFF;
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(route_bar());
         }
@@ -850,6 +877,70 @@ struct Kernel {
         }
     }
 
+    // 8-bit experts' x: a task is 512 columns of a token, whose whole row it reads for the scale.  The last
+    // blocks take them first, those which the scores leave idle.
+    __device__ void convert_x(float* red, const Me& me) {
+        const int parts = ceil_div(p.d, 512), nv = p.d / 8, tid = threadIdx.x;
+        const uint4* x = static_cast<const uint4*>(p.x);
+        for (int task = G - 1 - blockIdx.x; task < parts * p.T; task += G) {
+            const int t = task / parts, j = task % parts;
+            float m = 0.f;
+            auto larger = [&](uint32_t w) {
+                const float a = fabsf(__uint_as_float(w << 16)), b = fabsf(__uint_as_float(w & 0xFFFF0000u));
+                if (a < INFINITY) m = fmaxf(m, a);              // neither infinity nor NaN
+                if (b < INFINITY) m = fmaxf(m, b);
+            };
+            for (int i = tid; i < nv; i += CONS) {
+                const uint4 v = __ldg(x + (size_t)t * nv + i);
+                larger(v.x); larger(v.y); larger(v.z); larger(v.w);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (me.lane == 0) red[me.warp] = m;
+            named_sync(1, CONS);
+            m = red[0];
+#pragma unroll
+            for (int w = 1; w < CONS_WARPS; ++w) m = fmaxf(m, red[w]);
+            const float f = f16_scale(m);
+            const int c = j * 512 + tid * 2;
+            if (c < p.d) {
+                const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.x) + (size_t)t * p.d + c));
+                const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+                *reinterpret_cast<__half2*>(p.x16 + (size_t)t * p.d + c) = h;
+            }
+            if (j == 0 && tid == 0) p.xf[t] = 1.0f / f;
+            named_sync(1, CONS);
+        }
+    }
+
+    // The rows of h of the 8-bit experts, in place: two bf16 parts -> two fp16 parts of h * f16_scale(largest).
+    __device__ void convert_h() {
+        const int nv = p.I / 8, rows = h_rows();
+        for (int i = blockIdx.x * CONS + threadIdx.x; i < rows * nv; i += G * CONS) {
+            const int row = i / nv;
+            uint4* hi = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.h) + (size_t)row * 2 * p.Hs) + i % nv;
+            uint4* lo = hi + p.Hs / 8;
+            const float f = f16_scale(__uint_as_float(__ldcg(p.hmax + row)));
+            const uint4 a = __ldcg(hi), b = __ldcg(lo);
+            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+            uint32_t ow[2][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                // the parts' sum has 16 bits and is exact
+                const float v0 = (__uint_as_float(aw[q] << 16) + __uint_as_float(bw[q] << 16)) * f;
+                const float v1 = (__uint_as_float(aw[q] & 0xFFFF0000u) + __uint_as_float(bw[q] & 0xFFFF0000u)) * f;
+                const __half2 h = __floats2half2_rn(v0, v1);
+                const float2 g = __half22float2(h);
+                const float r0 = v0 - g.x, r1 = v1 - g.y;       // infinite or NaN: no low part
+                const __half2 l = __floats2half2_rn(fabsf(r0) < INFINITY ? r0 : 0.f, fabsf(r1) < INFINITY ? r1 : 0.f);
+                ow[0][q] = *reinterpret_cast<const uint32_t*>(&h);
+                ow[1][q] = *reinterpret_cast<const uint32_t*>(&l);
+            }
+            __stcg(hi, make_uint4(ow[0][0], ow[0][1], ow[0][2], ow[0][3]));
+            __stcg(lo, make_uint4(ow[1][0], ow[1][1], ow[1][2], ow[1][3]));
+        }
+    }
+
     __device__ __forceinline__ float bias_at(const void* b, size_t i) const { return to_f32(static_cast<const T*>(b)[i]); }
     __device__ __forceinline__ float gate_of(const Group& q, int tok) const {
         return q.shared ? 1.f : at<float>(L.gates)[q.row + __popc(q.mask & ((1u << tok) - 1u))];
@@ -882,28 +973,45 @@ struct Kernel {
 
     // Scales and biases of a unit's fragment, for the lane's row of w1 and of w3: loaded before the unit.
     struct Fin {
-        float s1, s3, b1, b3;
+        float s1, s3, b1, b3, x[2];                             // x: what undoes the scale of the lane's tokens' rows
     };
-    __device__ __forceinline__ Fin fin_of(const Group& q, int r) const {
-        Fin f = {1.f, 1.f, 0.f, 0.f};
+    __device__ __forceinline__ Fin fin_of(const Group& q, int r, int nt, int lane) const {
+        Fin f = {1.f, 1.f, 0.f, 0.f, {1.f, 1.f}};
         const int I = q.shared ? p.Is : p.I;
         if (r >= I) return f;
         const FfnWeights& W = q.shared ? p.Sh : p.R;
         const size_t at_row = (size_t)q.e * I + r;
         if (FR == W_E4M3 && !q.shared) { f.s1 = W.s1[at_row]; f.s3 = W.s3[at_row]; }
+        if (Q8 && !q.shared)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int tok = nt * 8 + (lane & 3) * 2 + i;
+                if (tok < p.T) f.x[i] = __ldcg(p.xf + tok);
+            }
         if (p.bias) { f.b1 = bias_at(W.b1, at_row); f.b3 = bias_at(W.b3, at_row); }
         return f;
     }
 
     // h of one unit's row r from the summed fragment (token group nt).
     __device__ __forceinline__ void finish_up(const Group& q, int r, const Fin& f, float4 c, int nt, int lane) {
-        if (r >= (q.shared ? p.Is : p.I)) return;
+        const bool in = r < (q.shared ? p.Is : p.I);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int tok = nt * 8 + (lane & 3) * 2 + i;
-            if (!((q.mask >> tok) & 1u)) continue;
-            const float a = (i ? c.y : c.x) * f.s1 + f.b1, b = (i ? c.w : c.z) * f.s3 + f.b3;
-            const float h = silu_f32(a) * b * gate_of(q, tok);
+            const bool mine = in && ((q.mask >> tok) & 1u);
+            float h = 0.f;
+            if (mine) {
+                // the weights' scale first: codes times scaled rows may lie beyond fp32's range of the result
+                const float a = (i ? c.y : c.x) * f.s1 * f.x[i] + f.b1, b = (i ? c.w : c.z) * f.s3 * f.x[i] + f.b3;
+                h = silu_f32(a) * b * gate_of(q, tok);
+            }
+            if (Q8 && !q.shared) {                              // 8 rows of a token: lanes 4 apart
+                float m = fabsf(h) < INFINITY ? fabsf(h) : 0.f;
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                if (lane < 4 && m > 0.f) atomicMax(p.hmax + q.row + __popc(q.mask & ((1u << tok) - 1u)), __float_as_uint(m));
+            }
+            if (!mine) continue;
             const size_t row = q.row + __popc(q.mask & ((1u << tok) - 1u));
             if (FR == W_F32) {
                 static_cast<float*>(p.h)[row * p.Hs + r] = h;
@@ -966,26 +1074,35 @@ struct Kernel {
         if constexpr (F == W_F32) {
             unit_f32<NT>(acc[0], me, K, q.mask);
         } else {
-            if (F == W_E4M3) {                                  // per-row scales differ from expert to expert
-                float t[R][NT * 4], f[R][2];
-                const float* s2 = p.R.s2 + (size_t)q.e * p.d;
+            // A unit has its own sums: scales differ from expert to expert, and a weight that is infinite or NaN
+            // must not reach the tokens that did not pick the expert (0 times it is NaN).
+            float t[R][NT * 4], f[R][2], x[NT][2];
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
+            for (int i = 0; i < R; ++i) {
 #pragma unroll
-                    for (int j = 0; j < NT * 4; ++j) t[i][j] = 0.f;
+                for (int j = 0; j < NT * 4; ++j) t[i][j] = 0.f;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int r = cb * DOWN + i * 16 + h * 8 + (me.lane >> 2);
-                        f[i][h] = r < p.d ? s2[r] : 0.f;
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    const int r = cb * DOWN + i * 16 + h * 8 + (me.lane >> 2);
+                    f[i][h] = F == W_E4M3 && r < p.d ? p.R.s2[(size_t)q.e * p.d + r] : 1.f;
                 }
-                unit_mma<FR, F, NT, 2, R>(t, me, 0, K, q.mask);
+            }
 #pragma unroll
-                for (int i = 0; i < R; ++i)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < NT * 4; ++j) acc[i][j] = fmaf(t[i][j], f[i][(j >> 1) & 1], acc[i][j]);
-            } else {
-                unit_mma<FR, F, NT, 2, R>(acc, me, Stage<FR, R>::scales(p.T), K, q.mask);
+                for (int j = 0; j < 2; ++j) {
+                    const int tok = nt * 8 + (me.lane & 3) * 2 + j;
+                    const int row = q.row + __popc(q.mask & ((1u << tok) - 1u));
+                    x[nt][j] = 1.f;
+                    if (F != W_BF16 && ((q.mask >> tok) & 1u)) x[nt][j] = 1.0f / f16_scale(__uint_as_float(__ldcg(p.hmax + row)));
+                }
+            unit_mma<FR, F, NT, 2, R>(t, me, Stage<FR, R>::scales(p.T), K, q.mask);
+#pragma unroll
+            for (int j = 0; j < NT * 4; ++j) {
+                const int tok = j / 4 * 8 + (me.lane & 3) * 2 + (j & 1);
+                if (!((q.mask >> tok) & 1u)) continue;
+#pragma unroll
+                for (int i = 0; i < R; ++i) acc[i][j] = fmaf(t[i][j] * f[i][(j >> 1) & 1], x[j / 4][j & 1], acc[i][j]);
             }
         }
         if (b2) add_b2(acc, me, q, b);
@@ -1034,6 +1151,10 @@ struct Kernel {
         for (int i = blockIdx.x * CONS + threadIdx.x; i < cbs * FRAGS; i += G * CONS) p.cnt[i] = 0u;
         if (p.T == 1) scores<1>(reinterpret_cast<float*>(red0), me);
         else scores<4>(reinterpret_cast<float*>(red0), me);
+        if (Q8) {
+            for (int i = blockIdx.x * CONS + threadIdx.x; i < p.T * p.k; i += G * CONS) p.hmax[i] = 0u;
+            convert_x(reinterpret_cast<float*>(red0), me);
+        }
         named_sync(1, CONS);                                    // the block's scores are written
         if (threadIdx.x == 0) grid_arrive(p.bar);
 
@@ -1057,7 +1178,7 @@ struct Kernel {
             up_unit(u, q, r0);
             const int f = my_frag(me, turn), r = r0 + f / NT * 8 + (me.lane >> 2);
             Fin fin = {};
-            if (f >= 0) fin = fin_of(q, r);
+            if (f >= 0) fin = fin_of(q, r, f % NT, me.lane);
             if (FR != FS && !q.shared) up<FR>(me, q, buffer());
             else up<FS>(me, q, buffer());
             named_sync(1, CONS);
@@ -1068,9 +1189,19 @@ struct Kernel {
         named_sync(1, CONS);                                    // the block's h is written
         if (threadIdx.x == 0) {
             grid_arrive(p.bar + 1);
-            if (grid_wait(p.bar + 1, at<unsigned long long>(L.turns)[1], abort_flag(), p.err)) mbar_arrive(h_bar());
+            const bool all = grid_wait(p.bar + 1, at<unsigned long long>(L.turns)[1], abort_flag(), p.err);
+            if (all && !Q8) mbar_arrive(h_bar());
         }
         named_sync(1, CONS);
+        if (Q8) {
+            convert_h();
+            named_sync(1, CONS);
+            if (threadIdx.x == 0) {
+                grid_arrive(p.bar + 2);
+                if (grid_wait(p.bar + 2, at<unsigned long long>(L.turns)[2], abort_flag(), p.err)) mbar_arrive(h_bar());
+            }
+            named_sync(1, CONS);
+        }
 
         const int groups = p.Ks + met;
         if (groups == 0) {                                      // no shared expert, and no pick left
@@ -1116,9 +1247,9 @@ __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__
         mbar_init(k.h_bar(), 1);
         mbar_init(k.gate_bar(), 1);
         // this block has not arrived yet, so that the barriers' rounds cannot end before it has read them
-        for (int i = 0; i < 2; ++i) k.template at<unsigned long long>(k.L.turns)[i] = round_end(load_acquire(p.bar + i), gridDim.x);
+        for (int i = 0; i < 3; ++i) k.template at<unsigned long long>(k.L.turns)[i] = round_end(load_acquire(p.bar + i), gridDim.x);
         int* misc = k.template at<int>(k.L.misc);
-        misc[0] = misc[1] = misc[2] = misc[3] = 0;              // given up; experts met; scores complete; the consumers' view
+        misc[0] = misc[1] = misc[2] = misc[3] = misc[4] = 0;    // given up; experts met; scores complete; the consumers' view; rows
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -1132,7 +1263,7 @@ size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 constexpr int GRID_MAX = 256, MAX_FRAGS = 4;
 
 struct Layout {
-    size_t logits, h, part, cnt, total;
+    size_t logits, h, x16, xf, hmax, part, cnt, total;
     int Hs;
 };
 Layout few_layout(const Dims& D) {
@@ -1143,6 +1274,9 @@ Layout few_layout(const Dims& D) {
     size_t o = 256;
     L.logits = o; o += al256(T * D.E * 4);
     L.h = o; o += al256(T * (D.k + D.Ks) * L.Hs * 4);           // two bf16 parts, or fp32
+    L.x16 = o; o += D.q8 ? al256(T * D.d * 2) : 0;
+    L.xf = o; o += D.q8 ? al256(T * 4) : 0;
+    L.hmax = o; o += D.q8 ? al256(T * D.k * 4) : 0;
     L.part = o; o += al256((size_t)GRID_MAX * 2 * MAX_FRAGS * 32 * 16);
     L.cnt = o; o += al256((size_t)ceil_div(D.d, 16) * MAX_FRAGS * 4);
     L.total = o;
@@ -1196,6 +1330,9 @@ cudaError_t launch_few(const Dims& D, const void* x, const void* cen, const floa
     p.out = out; p.idx = idx; p.gate = gate; p.counts = counts;
     p.logits = reinterpret_cast<float*>(w + L.logits);
     p.h = w + L.h;
+    p.x16 = reinterpret_cast<__half*>(w + L.x16);
+    p.xf = reinterpret_cast<float*>(w + L.xf);
+    p.hmax = reinterpret_cast<unsigned*>(w + L.hmax);
     p.part = reinterpret_cast<float4*>(w + L.part);
     p.cnt = reinterpret_cast<unsigned*>(w + L.cnt);
     p.err = reinterpret_cast<uint32_t*>(w);

@@ -41,7 +41,7 @@ def _run(L, ws=None, x=None, **kw):
     return o
 
 
-def _check(L, o, x=None):
+def _check(L, o, x=None, tiny=0.0):
     x = L["x"] if x is None else x
     assert moe.check_device_error(o["ws"]) == 0
     idx, gate = o["idx"].cpu().numpy().astype(np.int64), o["gate"].cpu().numpy().astype(np.float64)
@@ -50,7 +50,7 @@ def _check(L, o, x=None):
     assert np.array_equal(o["counts"].cpu().numpy(), np.bincount(idx.reshape(-1), minlength=L["cfg"].n_experts))
     ref, bound = R.few_layer(x, o["idx"], o["gate"], L["routed"], L["shared"], L["cfg"].n_shared)
     err = (o["out"].double() - ref).abs()
-    tol = R.HALF[x.dtype] * (ref.abs() + bound) + bound
+    tol = R.HALF[x.dtype] * (ref.abs() + bound) + bound + tiny
     assert (err <= tol).all(), float((err / tol).max())
 
 
@@ -154,6 +154,47 @@ def test_infinite_rows_stay_in_their_rows():
     got = _run(L)["out"]
     keep = torch.arange(128, device="cuda") != 7
     assert torch.equal(got[:, keep], want[:, keep]) and not torch.isfinite(got[:, 7]).any()
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3", "mxfp8"])
+def test_an_infinite_expert_stays_with_the_tokens_that_picked_it(fmt):
+    L = _case(T=6, d=256, E=24, I=64, k=2, Ks=1, fmt=fmt)
+    o = _run(L)
+    e = int(o["idx"][0, 0])
+    hit = (o["idx"] == e).any(1)
+    assert hit.any() and not hit.all()
+    w = L["routed"]["w2"]
+    if fmt:
+        w[e] = 0x7F                                             # the code of NaN
+    else:
+        w[e] = float("inf")
+    got = _run(L)["out"]
+    assert torch.equal(got[~hit], o["out"][~hit]) and not torch.isfinite(got[hit]).any()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "mxfp8"])
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** -40, 2.0 ** 20, 2.0 ** 60])
+def test_fp8_rows_of_any_size(fmt, size):
+    # rows of very different sizes, and hidden rows far outside fp16's range
+    L = _case(T=5, d=272, E=8, I=48, k=3, fmt=fmt, bias=False)
+    L["x"] *= torch.tensor([[1.0], [2.0 ** -30], [size], [2.0 ** -8], [0.0]], device="cuda", dtype=BF)
+    L["centroids"].zero_()                                      # the same experts for all
+    # h of a row of 2^-100 is near 2^-200, below fp32's normal numbers, and may be lost whole: 3 experts * 48 hidden
+    # values of at most 2^-126 times weights below 1 are less than 2^-118
+    _check(L, _run(L), tiny=2.0 ** -118)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "mxfp8"])
+def test_fp8_infinite_and_nan_inputs_stay_in_their_token(fmt):
+    L = _case(T=5, d=272, E=8, I=48, k=3, fmt=fmt, bias=False)
+    L["centroids"].zero_()
+    want = _run(L)["out"]
+    x = L["x"].clone()
+    x[1, 7], x[3, 0] = float("inf"), float("nan")
+    o = _run(L, x=x)                                            # 0 * infinity: NaN scores, no picks
+    with pytest.raises(moe.MoeError):
+        moe.check_device_error(o["ws"])
+    assert torch.equal(o["out"][[0, 2, 4]], want[[0, 2, 4]])
 
 
 def test_workspace_outputs_and_rows_around():
