@@ -28,7 +28,7 @@
 // pipe idles.  Scales are applied to fp32 sums (block scales: each run of 32 has its own sum).  Activations are
 // not quantised: x is bf16 as given, and h is kept as the sum of two bf16 numbers (16 significant bits).
 // 8-bit codes become fp16, exactly and in one instruction a pair (bf16 takes four, and the conversions then
-// bound the kernel: 196 us instead of XX for the products of w1, w3 of 22 experts of 2048 x 7168).  Their
+// bound the kernel: 185 us instead of 165 for w1, w3 of 22 block-scaled experts of 2048 x 7168).  Their
 // activations are therefore fp16 too, each row times a power of two that brings its largest finite value into
 // [2^14, 2^15): x in one number (its 8 bits are kept down to 2^-28 of that, and 2^-40 of it is the largest error), h in
 // two (22 bits), for which the rows' largest values have to be known: one grid barrier more, behind which the
@@ -139,7 +139,7 @@ __device__ __forceinline__ void async_wait_all() { asm volatile("cp.async.wait_a
 
 __device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -147,7 +147,7 @@ __device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uin
 
 __device__ __forceinline__ void mma_f16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -210,102 +210,105 @@ struct Ring {
     }
 };
 
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-    return v;
-}
+__device__ __forceinline__ uint4 lds128(const char* a) { return *reinterpret_cast<const uint4*>(a); }
 
-// acc += 16 R weight rows x up to 8 NT tokens over the warp's columns kb .. < K of a stage, wk columns from its
-// start.  act[nt]: the thread's token's row in the stage (0: the token is not among the unit's); HL = 2: its low
-// part follows `low` bytes on.  Columns past K hold an earlier stage's bytes: both operands are zeroed.
+// A thread's fragments of a stage: 16 R weight rows and up to 8 NT tokens over the warp's columns, wk from the
+// stage's start and kb < K of all.  act[nt]: where the thread's token's row is in the stage (0: the token is not
+// among the unit's); HL = 2: its low part follows ACT bytes on.  Columns past K hold an earlier stage's bytes:
+// both operands are zeroed.  sf: the scale bytes of the warp's 2 runs.
 template <int FR, int F, int NT, int HL, int R>
-__device__ __forceinline__ void mma_stage(float (&acc)[R][NT * 4], uint32_t stage, const uint32_t (&act)[NT], int low,
-                                          uint32_t sfs, int wk, int kb, int K, uint32_t mask, int lane) {
+struct Frag {
     using L = Fmt<FR, F>;
-    const int g = lane >> 2, c = (lane & 3) * 8;
-    const uint32_t row = stage + g * L::PITCH;
+    static constexpr int STEPS = L::PER_WARP / 32;
+    using A = typename std::conditional<F == W_BF16, uint4, uint2>::type;
+    A a[STEPS][R][2];
+    uint4 b[STEPS][NT][HL];
     uint32_t sf[R][2];
-    if (F == W_MX) {                                            // 2 runs of 64 columns
+
+    __device__ __forceinline__ void load(const char* stage, const int (&act)[NT], int sfs, int wk, int kb, int K, int lane) {
+        const int g = lane >> 2, c = (lane & 3) * 8;
+        const char* row = stage + g * L::PITCH;
 #pragma unroll
-        for (int i = 0; i < R; ++i)
+        for (int s = 0; s < STEPS; ++s) {
+            const int k = wk + s * 32 + c;
+            const bool in = kb + s * 32 + c < K;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-                sf[i][h] = lds32(sfs + (i * 16 + h * 8 + g) * 16 + wk / 128 * 4) >> (wk / 64 % 2 * 16);
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int q = 0; q < HL; ++q)
+                    b[s][nt][q] = in && act[nt] ? *reinterpret_cast<const uint4*>(stage + act[nt] + q * ACT + k * 2) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    a[s][i][h] = in ? *reinterpret_cast<const A*>(row + (i * 16 + h * 8) * L::PITCH + k * L::esz) : A{};
+        }
+        if (F == W_MX) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    sf[i][h] = *reinterpret_cast<const uint32_t*>(stage + sfs + (i * 16 + h * 8 + g) * 16 + wk / 128 * 4) >> (wk / 64 % 2 * 16);
+        }
     }
+
+    // acc += weights x activations
+    __device__ __forceinline__ void multiply(float (&acc)[R][NT * 4], uint32_t mask) const {
 #pragma unroll
-    for (int s = 0; s < L::PER_WARP / 32; ++s) {
-        const int k = wk + s * 32 + c;
-        const bool in = kb + s * 32 + c < K;
-        uint4 b[NT][HL];
+        for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int q = 0; q < HL; ++q)
-                b[nt][q] = in && act[nt] ? lds128(act[nt] + q * low + k * 2) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const uint32_t at = row + i * 16 * L::PITCH + k * L::esz;
-            uint4 a0 = make_uint4(0, 0, 0, 0), a1 = make_uint4(0, 0, 0, 0);
-            if (in) {
-                if (F == W_BF16) {
-                    a0 = lds128(at);
-                    a1 = lds128(at + 8 * L::PITCH);
+            for (int i = 0; i < R; ++i) {
+                uint4 a0, a1;
+                if constexpr (F == W_BF16) {
+                    a0 = a[s][i][0];
+                    a1 = a[s][i][1];
                 } else {
-                    const uint2 q0 = lds64(at), q1 = lds64(at + 8 * L::PITCH);
-                    const uint2 l0 = f16_of_codes(q0.x), h0 = f16_of_codes(q0.y);
-                    const uint2 l1 = f16_of_codes(q1.x), h1 = f16_of_codes(q1.y);
+                    const uint2 l0 = f16_of_codes(a[s][i][0].x), h0 = f16_of_codes(a[s][i][0].y);
+                    const uint2 l1 = f16_of_codes(a[s][i][1].x), h1 = f16_of_codes(a[s][i][1].y);
                     a0 = make_uint4(l0.x, l0.y, h0.x, h0.y);
                     a1 = make_uint4(l1.x, l1.y, h1.x, h1.y);
                 }
-            }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                if (NT > 1 && ((mask >> (8 * nt)) & 0xFFu) == 0u) continue;
-                float t[4] = {0.f, 0.f, 0.f, 0.f};              // block scales: a run's own sum, scaled in fp32
-                float* to = F == W_MX ? t : acc[i] + nt * 4;
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (NT > 1 && ((mask >> (8 * nt)) & 0xFFu) == 0u) continue;
+                    // Block scales: a run's own sum, scaled in fp32.  8-bit weights: the low parts' sums too, half the
+                    // chain of products.
+                    float t[HL][4] = {};
 #pragma unroll
-                for (int q = 0; q < HL; ++q) {
-                    if (F == W_BF16) {
-                        mma_bf16(to, a0.x, a1.x, a0.y, a1.y, b[nt][q].x, b[nt][q].y);
-                        mma_bf16(to, a0.z, a1.z, a0.w, a1.w, b[nt][q].z, b[nt][q].w);
-                    } else {
-                        mma_f16(to, a0.x, a1.x, a0.y, a1.y, b[nt][q].x, b[nt][q].y);
-                        mma_f16(to, a0.z, a1.z, a0.w, a1.w, b[nt][q].z, b[nt][q].w);
+                    for (int q = 0; q < HL; ++q) {
+                        const uint4& v = b[s][nt][q];
+                        float* to = F == W_MX || (q > 0 && F != W_BF16) ? t[q] : acc[i] + nt * 4;
+                        if (F == W_BF16) {
+                            mma_bf16(to, a0.x, a1.x, a0.y, a1.y, v.x, v.y);
+                            mma_bf16(to, a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+                        } else {
+                            mma_f16(to, a0.x, a1.x, a0.y, a1.y, v.x, v.y);
+                            mma_f16(to, a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+                        }
+                    }
+                    const float f0 = F == W_MX ? scale_of_byte((sf[i][0] >> (8 * s)) & 0xFFu) : 1.f;
+                    const float f1 = F == W_MX ? scale_of_byte((sf[i][1] >> (8 * s)) & 0xFFu) : 1.f;
+#pragma unroll
+                    for (int j = 0; j < 4 && (F == W_MX || (HL > 1 && F != W_BF16)); ++j) {
+                        const float v = (F == W_MX ? t[0][j] : 0.f) + (HL > 1 ? t[HL - 1][j] : 0.f);
+                        acc[i][nt * 4 + j] = fmaf(v, j < 2 ? f0 : f1, acc[i][nt * 4 + j]);
                     }
                 }
-                if (F == W_MX) {
-                    const float f0 = scale_of_byte((sf[i][0] >> (8 * s)) & 0xFFu), f1 = scale_of_byte((sf[i][1] >> (8 * s)) & 0xFFu);
-                    acc[i][nt * 4] = fmaf(t[0], f0, acc[i][nt * 4]);
-                    acc[i][nt * 4 + 1] = fmaf(t[1], f0, acc[i][nt * 4 + 1]);
-                    acc[i][nt * 4 + 2] = fmaf(t[2], f1, acc[i][nt * 4 + 2]);
-                    acc[i][nt * 4 + 3] = fmaf(t[3], f1, acc[i][nt * 4 + 3]);
-                }
             }
-        }
     }
-}
+};
 
 // What a consumer thread needs besides the unit itself.
 struct Me {
     Ring ring;
+    const char* sm;                                             // where the ring starts
     int warp, lane;
     volatile int* abort_flag;
     uint32_t* err;
 };
 
-__device__ __forceinline__ void wait_full(Me& me) {
-    mbar_wait_limit(me.ring.full(), me.ring.phase, me.abort_flag, me.err, true, WAIT_NS);
+__device__ __forceinline__ void wait_full(const Me& me, const Ring& r) {
+    mbar_wait_limit(r.full(), r.phase, me.abort_flag, me.err, true, WAIT_NS);
 }
 __device__ __forceinline__ void release(Me& me) {
     __syncwarp();
@@ -325,16 +328,40 @@ __device__ __forceinline__ void unit_mma(float (&acc)[R][NT * 4], Me& me, int sf
         const int n = nt * 8 + (me.lane >> 2);
         act[nt] = (mask >> n) & 1u ? Stage<FR, R>::acts + __popc(mask & ((1u << n) - 1u)) * HL * ACT : 0;
     }
-    for (int k0 = 0; k0 < K; k0 += L::KS) {
-        wait_full(me);
-        if (k0 + wk < K) {
-            const uint32_t stage = me.ring.at();
-            uint32_t a[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) a[nt] = act[nt] ? stage + act[nt] : 0u;
-            mma_stage<FR, F, NT, HL, R>(acc, stage, a, ACT, stage + sfs, wk, k0 + wk, K, mask, me.lane);
+    // With 8-bit weights the latencies of a stage (shared memory, conversions, a chain of products), two warps a
+    // scheduler, take longer than its bytes: where the registers allow it (one part an activation), a stage's
+    // fragments are loaded while the one before is multiplied (126 us instead of 145 for the products of w1, w3
+    // of 22 e4m3 experts of 2048 x 7168; with two parts, or 16-bit weights, it spills and loses).
+    using Fr = Frag<FR, F, NT, HL, R>;
+    Ring ahead = me.ring;
+    auto fetch = [&](Fr& f, int k0) {
+        wait_full(me, ahead);
+        if (k0 + wk < K) f.load(me.sm + ahead.slot * ahead.stage, act, sfs, wk, k0 + wk, K, me.lane);
+        ahead.next();
+    };
+    if constexpr (F == W_BF16 || HL > 1) {
+        Fr f;
+        for (int k0 = 0; k0 < K; k0 += L::KS) {
+            fetch(f, k0);
+            if (k0 + wk < K) f.multiply(acc, mask);
+            release(me);
         }
-        release(me);
+    } else {
+        Fr f[2];
+        int k0 = 0;
+        auto step = [&](const Fr& now, Fr& next) {
+            if (k0 + L::KS < K) fetch(next, k0 + L::KS);
+            if (k0 + wk < K) now.multiply(acc, mask);
+            release(me);
+            k0 += L::KS;
+        };
+        fetch(f[0], 0);
+        while (true) {
+            step(f[0], f[1]);
+            if (k0 >= K) break;
+            step(f[1], f[0]);
+            if (k0 >= K) break;
+        }
     }
 }
 
@@ -345,8 +372,9 @@ __device__ __forceinline__ void unit_f32(float (&acc)[NT * 8], Me& me, int K, ui
     using L = Fmt<W_F32, W_F32>;
     const int row = me.lane >> 1, half = me.lane & 1;
     for (int k0 = 0; k0 < K; k0 += L::KS) {
-        wait_full(me);
-        const uint32_t a = me.ring.at() + row * L::PITCH, x = me.ring.at() + Stage<W_F32, 1>::acts;
+        wait_full(me, me.ring);
+        const char* a = me.sm + me.ring.slot * me.ring.stage + row * L::PITCH;
+        const char* x = me.sm + me.ring.slot * me.ring.stage + Stage<W_F32, 1>::acts;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int c = me.warp * L::PER_WARP + (q * 2 + half) * 4;
@@ -354,7 +382,7 @@ __device__ __forceinline__ void unit_f32(float (&acc)[NT * 8], Me& me, int K, ui
             const uint4 u = lds128(a + c * 4);
             const float w0 = __uint_as_float(u.x), w1 = __uint_as_float(u.y), w2 = __uint_as_float(u.z),
                         w3 = __uint_as_float(u.w);
-            uint32_t at = x + c * 4;
+            const char* at = x + c * 4;
 #pragma unroll
             for (int n = 0; n < NT * 8; ++n) {
                 if (!((mask >> n) & 1u)) continue;
@@ -941,7 +969,6 @@ struct Kernel {
         }
     }
 
-    __device__ __forceinline__ float bias_at(const void* b, size_t i) const { return to_f32(static_cast<const T*>(b)[i]); }
     __device__ __forceinline__ float gate_of(const Group& q, int tok) const {
         return q.shared ? 1.f : at<float>(L.gates)[q.row + __popc(q.mask & ((1u << tok) - 1u))];
     }
@@ -971,12 +998,16 @@ struct Kernel {
         }
     }
 
-    // Scales and biases of a unit's fragment, for the lane's row of w1 and of w3: loaded before the unit.
+    // Scales and biases of a unit's fragment, for the lane's row of w1 and of w3: loaded before the unit, and as
+    // they are, since the first use would wait for them (and every warp of the block for this one).
     struct Fin {
-        float s1, s3, b1, b3, x[2];                             // x: what undoes the scale of the lane's tokens' rows
+        float s1, s3, x[2];                                     // x: what undoes the scale of the lane's tokens' rows
+        T b1, b3;
     };
     __device__ __forceinline__ Fin fin_of(const Group& q, int r, int nt, int lane) const {
-        Fin f = {1.f, 1.f, 0.f, 0.f, {1.f, 1.f}};
+        Fin f;
+        f.s1 = f.s3 = f.x[0] = f.x[1] = 1.f;
+        f.b1 = f.b3 = from_f32<T>(0.f);
         const int I = q.shared ? p.Is : p.I;
         if (r >= I) return f;
         const FfnWeights& W = q.shared ? p.Sh : p.R;
@@ -988,7 +1019,7 @@ struct Kernel {
                 const int tok = nt * 8 + (lane & 3) * 2 + i;
                 if (tok < p.T) f.x[i] = __ldcg(p.xf + tok);
             }
-        if (p.bias) { f.b1 = bias_at(W.b1, at_row); f.b3 = bias_at(W.b3, at_row); }
+        if (p.bias) { f.b1 = static_cast<const T*>(W.b1)[at_row]; f.b3 = static_cast<const T*>(W.b3)[at_row]; }
         return f;
     }
 
@@ -1002,7 +1033,7 @@ struct Kernel {
             float h = 0.f;
             if (mine) {
                 // the weights' scale first: codes times scaled rows may lie beyond fp32's range of the result
-                const float a = (i ? c.y : c.x) * f.s1 * f.x[i] + f.b1, b = (i ? c.w : c.z) * f.s3 * f.x[i] + f.b3;
+                const float a = (i ? c.y : c.x) * f.s1 * f.x[i] + to_f32(f.b1), b = (i ? c.w : c.z) * f.s3 * f.x[i] + to_f32(f.b3);
                 h = silu_f32(a) * b * gate_of(q, tok);
             }
             if (Q8 && !q.shared) {                              // 8 rows of a token: lanes 4 apart
@@ -1029,7 +1060,7 @@ struct Kernel {
 
     // acc (put_frag's order, fp32: put_f32's) += gate * b2 of the group's expert, for the rows b2_of has loaded.
     struct B2 {
-        float b[R][2];
+        T b[R][2];
     };
     __device__ __forceinline__ B2 b2_of(const Me& me, const Group& q, int cb) const {
         const void* b2 = q.shared ? p.Sh.b2 : p.R.b2;
@@ -1039,7 +1070,8 @@ struct Kernel {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int r = cb * DOWN + (FR == W_F32 ? me.lane >> 1 : i * 16 + h * 8 + (me.lane >> 2));
-                o.b[i][h] = r < p.d ? bias_at(b2, (size_t)q.e * p.d + r) : 0.f;
+                o.b[i][h] = from_f32<T>(0.f);
+                if (r < p.d) o.b[i][h] = static_cast<const T*>(b2)[(size_t)q.e * p.d + r];
             }
         return o;
     }
@@ -1048,7 +1080,7 @@ struct Kernel {
             if (me.lane & 1) return;
 #pragma unroll
             for (int n = 0; n < NT * 8; ++n)
-                if ((q.mask >> n) & 1u) acc[0][n] = fmaf(gate_of(q, n), b.b[0][0], acc[0][n]);
+                if ((q.mask >> n) & 1u) acc[0][n] = fmaf(gate_of(q, n), to_f32(b.b[0][0]), acc[0][n]);
         } else {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -1060,7 +1092,7 @@ struct Kernel {
 #pragma unroll
                     for (int i = 0; i < R; ++i)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) acc[i][nt * 4 + h * 2 + j] = fmaf(gate, b.b[i][h], acc[i][nt * 4 + h * 2 + j]);
+                        for (int h = 0; h < 2; ++h) acc[i][nt * 4 + h * 2 + j] = fmaf(gate, to_f32(b.b[i][h]), acc[i][nt * 4 + h * 2 + j]);
                 }
         }
     }
@@ -1074,9 +1106,11 @@ struct Kernel {
         if constexpr (F == W_F32) {
             unit_f32<NT>(acc[0], me, K, q.mask);
         } else {
+            // (Loads before the unit are used after it, so that no warp waits for them.)
             // A unit has its own sums: scales differ from expert to expert, and a weight that is infinite or NaN
             // must not reach the tokens that did not pick the expert (0 times it is NaN).
-            float t[R][NT * 4], f[R][2], x[NT][2];
+            float t[R][NT * 4], f[R][2];
+            unsigned m[NT][2];
 #pragma unroll
             for (int i = 0; i < R; ++i) {
 #pragma unroll
@@ -1093,16 +1127,17 @@ struct Kernel {
                 for (int j = 0; j < 2; ++j) {
                     const int tok = nt * 8 + (me.lane & 3) * 2 + j;
                     const int row = q.row + __popc(q.mask & ((1u << tok) - 1u));
-                    x[nt][j] = 1.f;
-                    if (F != W_BF16 && ((q.mask >> tok) & 1u)) x[nt][j] = 1.0f / f16_scale(__uint_as_float(__ldcg(p.hmax + row)));
+                    m[nt][j] = 0u;
+                    if (F != W_BF16 && ((q.mask >> tok) & 1u)) m[nt][j] = __ldcg(p.hmax + row);
                 }
             unit_mma<FR, F, NT, 2, R>(t, me, Stage<FR, R>::scales(p.T), K, q.mask);
 #pragma unroll
             for (int j = 0; j < NT * 4; ++j) {
                 const int tok = j / 4 * 8 + (me.lane & 3) * 2 + (j & 1);
                 if (!((q.mask >> tok) & 1u)) continue;
+                const float x = F == W_BF16 ? 1.f : 1.0f / f16_scale(__uint_as_float(m[j / 4][j & 1]));
 #pragma unroll
-                for (int i = 0; i < R; ++i) acc[i][j] = fmaf(t[i][j] * f[i][(j >> 1) & 1], x[j / 4][j & 1], acc[i][j]);
+                for (int i = 0; i < R; ++i) acc[i][j] = fmaf(t[i][j] * f[i][(j >> 1) & 1], x, acc[i][j]);
             }
         }
         if (b2) add_b2(acc, me, q, b);
@@ -1145,7 +1180,7 @@ struct Kernel {
     }
 
     __device__ void consume() {
-        Me me = {ring(), (int)(threadIdx.x >> 5), (int)(threadIdx.x & 31), abort_flag(), p.err};
+        Me me = {ring(), sm + L.ring, (int)(threadIdx.x >> 5), (int)(threadIdx.x & 31), abort_flag(), p.err};
         float4* red0 = at<float4>(L.red);
         const int cbs = ceil_div(p.d, DOWN);
         for (int i = blockIdx.x * CONS + threadIdx.x; i < cbs * FRAGS; i += G * CONS) p.cnt[i] = 0u;
