@@ -211,7 +211,13 @@ FfnWeights to_ffn(const moe_ffn_weights_t* w) {
     return f;
 }
 
-// e4m3 routed experts: x quantised once per token, then its code rows (and scales) gathered
+// x in 8 bits as the caller has it: [T][d] codes, and fp32 [T] scales or (block-scaled) [T][ceil(d / 32)] bytes.
+struct QuantX {
+    const uint8_t* codes;
+    const void* scales;
+};
+
+// e4m3 routed experts: x quantised once per token (unless given), then its code rows (and scales) gathered
 // into expert order for the GEMM1 A operand.
 // With the slot map at hand (the fused forward) the code rows are written in token order
 // instead: each token's codes are read once and stored at its k slot positions.
@@ -219,19 +225,27 @@ FfnWeights to_ffn(const moe_ffn_weights_t* w) {
 // layout by grouped position (needs the tile table ts1).
 moe_status_t quant_gather_x(const Dims& D, const Layout& L, void* ws, const void* x, const int32_t* stok,
                             const int32_t* offsets, const int32_t* ts1, uint32_t* err, cudaStream_t st,
-                            const int32_t* slot_of = nullptr) {
-    uint8_t* x8t = at<uint8_t>(ws, L.x8t);
-    float* xst = D.mx ? nullptr : at<float>(ws, L.xst);
+                            const int32_t* slot_of = nullptr, const QuantX* given = nullptr) {
+    const uint8_t* x8t = at<uint8_t>(ws, L.x8t);
+    const float* xst = D.mx ? nullptr : at<float>(ws, L.xst);
+    const uint8_t* xsf = at<uint8_t>(ws, L.xsf);
     float* xs = D.mx ? nullptr : at<float>(ws, L.xs);
-    if (D.mx) MOE_CUDA(launch_quant_rows_mx(x, D.T, D.d, x8t, at<uint8_t>(ws, L.xsf), st));
-    else MOE_CUDA(launch_quant_rows(x, nullptr, D.T, D.T, D.d, x8t, xst, err, st));
+    if (given) {
+        x8t = given->codes;
+        if (D.mx) xsf = static_cast<const uint8_t*>(given->scales);
+        else xst = static_cast<const float*>(given->scales);
+    } else if (D.mx) {
+        MOE_CUDA(launch_quant_rows_mx(x, D.T, D.d, at<uint8_t>(ws, L.x8t), at<uint8_t>(ws, L.xsf), st));
+    } else {
+        MOE_CUDA(launch_quant_rows(x, nullptr, D.T, D.T, D.d, at<uint8_t>(ws, L.x8t), at<float>(ws, L.xst), err, st));
+    }
     if (slot_of)
         MOE_CUDA(launch_scatter_code_rows(x8t, xst, slot_of, D.T, D.k, D.slots(), D.d, at<uint8_t>(ws, L.xperm), xs,
                                           err, st));
     else
         MOE_CUDA(launch_gather_code_rows(x8t, xst, stok, D.slots(), D.T, D.d, at<uint8_t>(ws, L.xperm), xs, err, st));
     if (D.mx)
-        MOE_CUDA(launch_scatter_sf_tiled(at<uint8_t>(ws, L.xsf), D.T, D.d, stok, offsets, ts1, D.E, D.slots(), D.I,
+        MOE_CUDA(launch_scatter_sf_tiled(xsf, D.T, D.d, stok, offsets, ts1, D.E, D.slots(), D.I,
                                          at<uint8_t>(ws, L.sfa1), err, st));
     return MOE_OK;
 }
@@ -498,7 +512,7 @@ moe_status_t layer_forward_impl(const moe_shape_t* shape, const void* x, const v
                                 const float* router_bias, const moe_ffn_weights_t* routed, const moe_ffn_weights_t* shared, void* out,
                                 int32_t* topk_idx_out, float* topk_gate_out, int32_t* counts_out, void* ws,
                                 size_t ws_bytes, cudaStream_t st, cudaEvent_t const* ev, void* ctx = nullptr,
-                                size_t ctx_bytes = 0) {
+                                size_t ctx_bytes = 0, const QuantX* xq = nullptr) {
     Dims D;
     MOE_TRY(to_dims(shape, &D));
     if (!centroids || (D.T > 0 && (!x || !out))) return MOE_ERR_INVALID_ARG;
@@ -506,6 +520,11 @@ moe_status_t layer_forward_impl(const moe_shape_t* shape, const void* x, const v
     if (D.Ks > 0) MOE_TRY(check_weights(D, shared));
     else if (shared) return MOE_ERR_INVALID_ARG;
     MOE_TRY(check_ws(D, ws, ws_bytes));
+    if (xq) {
+        if (!D.q8) return MOE_ERR_UNSUPPORTED;
+        if (D.T > 0 && (!xq->codes || !xq->scales)) return MOE_ERR_INVALID_ARG;
+        if (((uintptr_t)xq->codes & 15u) || (!D.mx && ((uintptr_t)xq->scales & 3u))) return MOE_ERR_INVALID_ARG;
+    }
     if (ctx) {
         MOE_TRY(check_train(D));
         if (ctx_bytes < ctx_layout(D).total || ((uintptr_t)ctx & 15u)) return MOE_ERR_WORKSPACE;
@@ -548,7 +567,7 @@ moe_status_t layer_forward_impl(const moe_shape_t* shape, const void* x, const v
     if (D.q8) {
         uint8_t* x8 = at<uint8_t>(ws, L.xperm);
         float* xs = D.mx ? nullptr : at<float>(ws, L.xs);
-        MOE_TRY(quant_gather_x(D, L, ws, x, stok, offsets, ts1, err, st, slot_of));
+        MOE_TRY(quant_gather_x(D, L, ws, x, stok, offsets, ts1, err, st, slot_of, xq));
         if (!mark(4)) return MOE_ERR_CUDA;
         const MxAct m1 = mx_gemm1(L, ws), m2 = mx_gemm2(L, ws);
         MOE_CUDA(launch_tc_gemm1_q8(D, x, x8, xs, offsets, ts1, R, Sh, hr, hs, D.E + D.Ks, err, st,
@@ -707,6 +726,16 @@ MOE_EXPORT moe_status_t moe_layer_forward(const moe_shape_t* shape, const void* 
                                           size_t ws_bytes, moe_stream_t stream) {
     return layer_forward_impl(shape, x, centroids, router_bias, routed, shared, out, topk_idx_out, topk_gate_out,
                               counts_out, ws, ws_bytes, (cudaStream_t)stream, nullptr);
+}
+
+MOE_EXPORT moe_status_t moe_layer_forward_quantized(const moe_shape_t* shape, const void* x, const uint8_t* x_codes,
+                                                    const void* x_scales, const void* centroids, const float* router_bias,
+                                                    const moe_ffn_weights_t* routed, const moe_ffn_weights_t* shared,
+                                                    void* out, int32_t* topk_idx_out, float* topk_gate_out,
+                                                    int32_t* counts_out, void* ws, size_t ws_bytes, moe_stream_t stream) {
+    const QuantX xq = {x_codes, x_scales};
+    return layer_forward_impl(shape, x, centroids, router_bias, routed, shared, out, topk_idx_out, topk_gate_out,
+                              counts_out, ws, ws_bytes, (cudaStream_t)stream, nullptr, nullptr, 0, &xq);
 }
 
 MOE_EXPORT moe_status_t moe_layer_forward_timed(const moe_shape_t* shape, const void* x, const void* centroids,

@@ -29,7 +29,7 @@ EXPORTED = ("moe_workspace_bytes", "moe_layer_launches", "moe_status_string", "m
             "moe_balance_stats", "moe_gather_rows", "moe_segment_ids", "moe_selftest_wait_timeout",
             "moe_mx_scale_bytes", "moe_quantize_weights_mx", "moe_rmsnorm", "moe_rmsnorm_backward",
             "moe_rmsnorm_backward_workspace_bytes", "moe_grad_workspace_bytes", "moe_grad_norm", "moe_clip_grads",
-            "moe_few_workspace_bytes", "moe_layer_forward_few")
+            "moe_few_workspace_bytes", "moe_layer_forward_few", "moe_layer_forward_quantized")
 FEW_MAX_TOKENS = 16                          # MOE_FEW_MAX_TOKENS
 NUM_STAGES = 7
 STAGE_NAMES = ("router", "permute", "plan", "gather", "gemm1_swiglu", "gemm2", "combine")
@@ -128,7 +128,9 @@ def _lib():
         lib.moe_few_workspace_bytes.argtypes = [sh]
         lib.moe_few_workspace_bytes.restype = sz
         lib.moe_layer_forward_few.argtypes = lib.moe_layer_forward.argtypes
-        for n in ("moe_rmsnorm", "moe_rmsnorm_backward", "moe_grad_norm", "moe_clip_grads", "moe_layer_forward_few"):
+        lib.moe_layer_forward_quantized.argtypes = lib.moe_layer_forward.argtypes[:2] + [vp, vp] + lib.moe_layer_forward.argtypes[2:]
+        for n in ("moe_rmsnorm", "moe_rmsnorm_backward", "moe_grad_norm", "moe_clip_grads", "moe_layer_forward_few",
+                  "moe_layer_forward_quantized"):
             getattr(lib, n).restype = ctypes.c_int
         for n in ("moe_check_device_error", "moe_ws_init", "moe_route", "moe_permute", "moe_expert_ffn",
                   "moe_combine", "moe_layer_forward", "moe_layer_forward_timed", "moe_quantize_rows_e4m3",
@@ -380,6 +382,33 @@ def layer_forward(shape: MoeShape, x, centroids, routed: Dict, shared: Optional[
     _check(_lib().moe_layer_forward(ctypes.byref(shape), _ptr(x), _ptr(centroids), _bias_ptr(router_bias), ctypes.byref(rw),
                                     None if sw is None else ctypes.byref(sw), _ptr(out), _ptr(idx), _ptr(gate),
                                     _ptr(counts), _ptr(ws), ws.numel(), _stream(stream)), "moe_layer_forward")
+    return out
+
+
+def layer_forward_quantized(shape: MoeShape, x, x_codes, x_scale, centroids, routed: Dict, shared: Optional[Dict], ws,
+                            out=None, idx=None, gate=None, counts=None, stream=None, router_bias=None):
+    """layer_forward for FP8 routed experts with x in 8 bits at hand (moe_layer_forward_quantized): x_codes and x_scale as
+    rmsnorm returns them ("codes", "scale") in the routed experts' format."""
+    dev = _need_layer(shape, x, centroids, routed, shared, out, idx, gate, counts, router_bias)
+    if shape.routed_fmt not in (FMT_E4M3, FMT_MXFP8):
+        raise ValueError("x in 8 bits needs 8-bit routed experts")
+    if x_codes is None or x_scale is None:
+        raise TypeError("x_codes and x_scale must be torch.Tensors")
+    _need(x_codes, "x_codes", shape.T * shape.d, torch.uint8, dev)
+    if shape.routed_fmt == FMT_E4M3:
+        _need(x_scale, "x_scale", shape.T, torch.float32, dev)
+    else:
+        _need(x_scale, "x_scale", shape.T * (-(-shape.d // 32)), torch.uint8, dev)
+    _need(ws, "ws", 0, torch.uint8, dev)
+    _on_cuda(dev)
+    out = torch.empty((shape.T, shape.d), dtype=x.dtype, device=dev) if out is None else out
+    rw, sw = _weights(routed), _weights(shared)
+    with _device_of(dev):
+        _check(_lib().moe_layer_forward_quantized(ctypes.byref(shape), _ptr(x), _ptr(x_codes), _ptr(x_scale), _ptr(centroids),
+                                                  _bias_ptr(router_bias), ctypes.byref(rw),
+                                                  None if sw is None else ctypes.byref(sw), _ptr(out), _ptr(idx), _ptr(gate),
+                                                  _ptr(counts), _ptr(ws), ws.numel(), _stream_of(dev, stream)),
+               "moe_layer_forward_quantized")
     return out
 
 

@@ -513,6 +513,20 @@ moe_status_t moe_rmsnorm_backward(int32_t dtype, int64_t rows, int32_t d, const 
                                   const void* weight, const float* rstd, const void* dsum, void* dx, float* dweight,
                                   void* ws, size_t ws_bytes, moe_stream_t stream);
 
+/*
+ * moe_layer_forward for FP8 routed experts whose input rows are already in 8 bits: as moe_rmsnorm writes
+ * them in the routed experts' format (or moe_quantize_rows_e4m3), so that the layer does not quantise x again.
+ *   x: the 16-bit rows all the same, which the router and the shared experts read
+ *   x_codes [T, d], 16-byte aligned; x_scales: fp32 [T] (MOE_FMT_E4M3) or bytes [T, ceil(d / 32)] (MOE_FMT_MXFP8)
+ * All else is as in moe_layer_forward, with the same workspace; with the codes and scales that it would make
+ * of x itself the results are the same bits.  MOE_ERR_UNSUPPORTED unless routed_fmt is an 8-bit format.
+ */
+moe_status_t moe_layer_forward_quantized(const moe_shape_t* shape, const void* x, const uint8_t* x_codes,
+                                         const void* x_scales, const void* centroids, const float* router_bias,
+                                         const moe_ffn_weights_t* routed, const moe_ffn_weights_t* shared, void* out,
+                                         int32_t* topk_idx_out, float* topk_gate_out, int32_t* counts_out, void* ws,
+                                         size_t ws_bytes, moe_stream_t stream);
+
 /* One tensor of a list: `numel` consecutive elements of dtype at `data` (any alignment its type allows). */
 typedef struct {
     void* data;
@@ -545,7 +559,8 @@ moe_status_t moe_clip_grads(const moe_tensor_t* grads, const moe_tensor_t* out, 
  * With FP8 routed experts (MOE_FMT_E4M3, MOE_FMT_MXFP8) the weights are the codes times their scales, as
  * everywhere, but the activations are NOT quantised: with few tokens nothing is gained by it, and the
  * result is the layer's on the dequantised weights.  So it can differ from moe_layer_forward's, which
- * quantises them, by that quantisation.  Hidden values keep 16 significant bits (fp32 layers: 24); sums are
+ * quantises them, by that quantisation.  Hidden values keep 16 significant bits (fp32 layers: 24); for FP8
+ * experts a row of x or of hidden values is accurate to 2^-40 of its largest value at least.  Sums are
  * fp32, in an order that depends on sizes and picks alone.
  * A pick that does not exist (NaN logits, or all other keys -infinity) sets error bit 1 and is left out.
  * Sizes: as the layer's, T <= MOE_FEW_MAX_TOKENS, d <= 32768, and for MOE_F32 d, inter and inter_shared
