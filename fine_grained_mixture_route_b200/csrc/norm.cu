@@ -188,10 +188,10 @@ __global__ void __launch_bounds__(VPT <= 2 || VEC == 1 ? 1024 : 512)
 // Backward.  Blocks (or, with WARP, the 8 warps of a block) walk the rows; each thread keeps its
 // columns' share of dweight in registers, and a block writes one row of partial sums.
 template <typename T, int VEC, int VPT, bool WARP, bool DSUM>
-__global__ void __launch_bounds__(VEC == 1 && !WARP ? 1024 : (VPT <= 2 && !WARP ? 1024 : 512))
-    rmsnorm_bwd_kernel(const T* __restrict__ dy, const T* __restrict__ s, const T* __restrict__ w,
-                       const float* __restrict__ rstd, const T* __restrict__ dsum, long long rows, int d,
-                       T* __restrict__ dx, float* __restrict__ partial) {
+__global__ void __launch_bounds__(WARP ? 256 : VEC == 1 || VPT <= 2 ? 1024 : 512)
+    rmsnorm_bwd_kernel(const T* dy, const T* __restrict__ s, const T* __restrict__ w,
+                       const float* __restrict__ rstd, const T* dsum, long long rows, int d, T* dx,
+                       float* __restrict__ partial) {
     using P = Pack<T, VEC>;
     extern __shared__ float smw[];                             // WARP: [warps][d] partial sums
     __shared__ float2 sm[2][32];
@@ -211,27 +211,50 @@ __global__ void __launch_bounds__(VEC == 1 && !WARP ? 1024 : (VPT <= 2 && !WARP 
         for (int e = 0; e < VEC; ++e) acc[j][e] = 0.f;
     }
     const long long step = WARP ? (long long)gridDim.x * nw : (long long)gridDim.x;
+    const long long row0 = WARP ? (long long)blockIdx.x * nw + warp : (long long)blockIdx.x;
+    // One vector a thread: a row is loaded while the one before is reduced and written, as otherwise the memory
+    // idles during the reductions (16384 rows of 7168: 191 us with two vectors a thread and no loads ahead, 164 us so).
+    constexpr bool AHEAD = VEC > 1 && VPT == 1;
+    P na, nb, nc;
+    float nr = 0.f;
+    auto ahead = [&](long long row) {
+        if (row >= rows || me >= nv) return;
+        na = reinterpret_cast<const P*>(s + (size_t)row * d)[me];
+        nb = reinterpret_cast<const P*>(dy + (size_t)row * d)[me];
+        if (DSUM) nc = reinterpret_cast<const P*>(dsum + (size_t)row * d)[me];
+        nr = rstd[row];
+    };
+    if (AHEAD) {
+        na.zero(); nb.zero(); nc.zero();
+        ahead(row0);
+    }
     int turn = 0;
-    for (long long row = WARP ? (long long)blockIdx.x * nw + warp : (long long)blockIdx.x; row < rows; row += step, turn ^= 1) {
+    for (long long row = row0; row < rows; row += step, turn ^= 1) {
         const P* sr = reinterpret_cast<const P*>(s + (size_t)row * d);
         const P* gr = reinterpret_cast<const P*>(dy + (size_t)row * d);
         P a[VPT], b[VPT], c[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int i = me + j * width;
-            if (i < nv) { a[j] = sr[i]; b[j] = gr[i]; }
-            else { a[j].zero(); b[j].zero(); }
-        }
-        if (DSUM) {
-            const P* qr = reinterpret_cast<const P*>(dsum + (size_t)row * d);
+        float r;
+        if (AHEAD) {
+            a[0] = na; b[0] = nb; c[0] = nc; r = nr;
+            ahead(row + step);
+        } else {
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int i = me + j * width;
-                if (i < nv) c[j] = qr[i];
-                else c[j].zero();
+                if (i < nv) { a[j] = sr[i]; b[j] = gr[i]; }
+                else { a[j].zero(); b[j].zero(); }
             }
+            if (DSUM) {
+                const P* qr = reinterpret_cast<const P*>(dsum + (size_t)row * d);
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    const int i = me + j * width;
+                    if (i < nv) c[j] = qr[i];
+                    else c[j].zero();
+                }
+            }
+            r = rstd[row];
         }
-        const float r = rstd[row];
         float dot = 0.f, none = 0.f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
@@ -336,9 +359,12 @@ cudaError_t norm_shape(const NormArgs& a, cudaStream_t st) {
     if (!few && nv <= 32) return norm_res<T, VEC, 1, true, FMT>(a, 256, st);
     if (!few && nv <= 128) return norm_res<T, VEC, 4, true, FMT>(a, 256, st);
     if (few && nv <= 1024) return norm_res<T, VEC, 1, false, FMT>(a, round32(nv), st);
-    if (nv <= 2048) return norm_res<T, VEC, 4, false, FMT>(a, round32((nv + 3) / 4), st);
-    if (VEC > 1) return norm_res<T, VEC, 8, false, FMT>(a, round32((nv + 7) / 8), st);
-    return norm_res<T, VEC, 16, false, FMT>(a, round32((nv + 15) / 16), st);
+    if (VEC == 8 || nv <= 2048) return norm_res<T, VEC, 4, false, FMT>(a, round32((nv + 3) / 4), st);
+    if constexpr (VEC < 8) {                                   // fp32: 16384 columns are 4096 vectors, or 16384 single ones
+        if (VEC > 1 || nv <= 8192) return norm_res<T, VEC, 8, false, FMT>(a, round32((nv + 7) / 8), st);
+        return norm_res<T, VEC, VEC == 1 ? 16 : 8, false, FMT>(a, round32((nv + 15) / 16), st);
+    }
+    return cudaErrorInvalidValue;
 }
 
 struct BwdArgs {
@@ -365,14 +391,22 @@ cudaError_t bwd_shape(const BwdArgs& a, int* blocks, cudaStream_t st) {
     const int nv = a.d / VEC;
     const int cap = norm_bwd_partials(a.rows);
     *blocks = (int)(a.rows < cap ? a.rows : cap);
-    if (nv <= 32 || nv <= 128) {                               // 8 warps of a block, a row each
+    if (nv <= 128) {                               // 8 warps of a block, a row each
         *blocks = (int)((a.rows + 7) / 8 < cap ? (a.rows + 7) / 8 : cap);
         return nv <= 32 ? bwd_launch<T, VEC, 1, true>(a, 256, *blocks, st)
                         : bwd_launch<T, VEC, 4, true>(a, 256, *blocks, st);
     }
-    if (nv <= 2048) return bwd_launch<T, VEC, 2, false>(a, round32((nv + 1) / 2), *blocks, st);
-    if (VEC > 1) return bwd_launch<T, VEC, 8, false>(a, round32((nv + 7) / 8), *blocks, st);
-    return bwd_launch<T, VEC, 16, false>(a, round32((nv + 15) / 16), *blocks, st);
+    if (VEC > 1 && nv <= 1024) {                               // as many blocks as fit, with 64 registers a thread
+        const int threads = round32(nv), fit = num_sms() * (1024 / threads);
+        if (*blocks > fit) *blocks = fit;
+        return bwd_launch<T, VEC, 1, false>(a, threads, *blocks, st);
+    }
+    if (VEC == 8 || nv <= 2048) return bwd_launch<T, VEC, 2, false>(a, round32((nv + 1) / 2), *blocks, st);
+    if constexpr (VEC < 8) {                                   // fp32: 16384 columns are 4096 vectors, or 16384 single ones
+        if (VEC > 1 || nv <= 8192) return bwd_launch<T, VEC, 8, false>(a, round32((nv + 7) / 8), *blocks, st);
+        return bwd_launch<T, VEC, VEC == 1 ? 16 : 8, false>(a, round32((nv + 15) / 16), *blocks, st);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
