@@ -6,6 +6,7 @@ shared library is missing or the device is not a B200, calls raise.
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import os
@@ -147,7 +148,7 @@ def lib_handle():
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
@@ -227,11 +228,14 @@ def _need_stack(w: Optional[Dict], name: str, shape: MoeShape, shared: bool, dev
     wdt = torch.uint8 if codes else dt
     for k, n, kdt in (("w1", E * I * d, wdt), ("w3", E * I * d, wdt), ("w2", E * d * I, wdt),
                       ("b1", E * I, dt), ("b3", E * I, dt), ("b2", E * d, dt),
-                      ("s1", E * I, torch.float32), ("s3", E * I, torch.float32), ("s2", E * d, torch.float32),
-                      ("sf13", mx_scale_bytes(MX_UP, E, I, d), torch.uint8),
-                      ("sf2", mx_scale_bytes(MX_DOWN, E, d, I), torch.uint8)):
-        if k in w:
-            _need(w[k], f"{name}.{k}", n, kdt, device)
+                      ("s1", E * I, torch.float32), ("s3", E * I, torch.float32), ("s2", E * d, torch.float32)):
+        t = w.get(k)
+        if t is not None:
+            _need(t, f"{name}.{k}", n, kdt, device)
+    if w.get("sf13") is not None:
+        _need(w["sf13"], f"{name}.sf13", mx_scale_bytes(MX_UP, E, I, d), torch.uint8, device)
+    if w.get("sf2") is not None:
+        _need(w["sf2"], f"{name}.sf2", mx_scale_bytes(MX_DOWN, E, d, I), torch.uint8, device)
 
 
 def _bias_ptr(router_bias: Optional[torch.Tensor]):
@@ -245,10 +249,12 @@ def _bias_ptr(router_bias: Optional[torch.Tensor]):
 def _weights(w: Optional[Dict]):
     if w is None:
         return None
-    for k in ("w1", "w3", "w2", "b1", "b3", "b2", "s1", "s3", "s2", "sf13", "sf2"):
+    ptrs = []
+    for k in ("w1", "b1", "w3", "b3", "w2", "b2", "s1", "s3", "s2", "sf13", "sf2"):
         t = w.get(k)
         if t is not None and not t.is_contiguous():
             raise ValueError(f"weight {k} must be contiguous")
+        ptrs.append(None if t is None else t.data_ptr())
     if w["w1"].dtype == torch.uint8:
         if w.get("sf13") is not None:
             for k in ("sf13", "sf2"):
@@ -258,8 +264,7 @@ def _weights(w: Optional[Dict]):
             for k in ("s1", "s3", "s2"):
                 if w.get(k) is None or w[k].dtype != torch.float32:
                     raise ValueError(f"e4m3 weights need float32 scales {k}")
-    names = ("w1", "b1", "w3", "b3", "w2", "b2", "s1", "s3", "s2", "sf13", "sf2")
-    return MoeWeights(*(None if w.get(k) is None else w[k].data_ptr() for k in names))
+    return MoeWeights(*ptrs)
 
 
 def workspace_bytes(shape: MoeShape) -> int:
@@ -695,17 +700,13 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: 
             "codes": None if fmt == FMT_NATIVE else ((rows, d), torch.uint8),
             "scale": {FMT_NATIVE: None, FMT_E4M3: ((rows,), torch.float32),
                       FMT_MXFP8: ((rows, -(-d // 32)), torch.uint8)}[fmt]}
-    o = {}
-    for k, spec in want.items():
-        given = None if out is None else out.get(k)
-        if spec is None:
-            o[k] = None
-        elif given is not None:
-            _exactly(given, f"out[{k!r}]", spec[0], spec[1], dev)
-            o[k] = given
+    o = dict.fromkeys(want) if out is None else {k: out.get(k) if spec else None for k, spec in want.items()}
+    for k, t in o.items():
+        if t is not None:
+            _exactly(t, f"out[{k!r}]", want[k][0], want[k][1], dev)
     _on_cuda(dev)
     for k, spec in want.items():
-        if k not in o:
+        if spec is not None and o[k] is None:
             o[k] = torch.empty(spec[0], dtype=spec[1], device=dev)
     with _device_of(dev):
         _check(_lib().moe_rmsnorm(MOE_BF16 if dt == torch.bfloat16 else MOE_F32, rows, d, _ptr(x), _ptr(residual),
@@ -762,17 +763,30 @@ def new_grad_workspace(device="cuda") -> torch.Tensor:
 
 
 def _tensor_list(tensors, name: str, device: torch.device):
+    """(descriptors for the C entry points, [(first byte, end, index)] of the tensors that hold elements)."""
+    flat, spans = array.array("q"), []                          # moe_tensor_t: pointer, int64, int32 and padding
     for i, t in enumerate(tensors):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}[{i}] must be a torch.Tensor")
-        if t.dtype not in (torch.bfloat16, torch.float32):
-            raise ValueError(f"{name}[{i}] has dtype {t.dtype}; bfloat16 or float32 is needed")
+        dt = t.dtype
+        if dt != torch.bfloat16 and dt != torch.float32:
+            raise ValueError(f"{name}[{i}] has dtype {dt}; bfloat16 or float32 is needed")
         if not t.is_contiguous():
             raise ValueError(f"{name}[{i}] must be contiguous")
         if t.device != device:
             raise ValueError(f"{name}[{i}] is on {t.device}; the workspace is on {device}")
-    return (MoeTensor * max(len(tensors), 1))(
-        *(MoeTensor(t.data_ptr(), t.numel(), MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32) for t in tensors))
+        p, n = t.data_ptr(), t.numel()
+        if dt == torch.bfloat16:
+            flat.extend((p, n, MOE_BF16))
+            end = p + 2 * n
+        else:
+            flat.extend((p, n, MOE_F32))
+            end = p + 4 * n
+        if n:
+            spans.append((p, end, i))
+    if not flat:
+        flat.extend((0, 0, 0))
+    return (MoeTensor * (len(flat) // 3)).from_buffer(flat), spans
 
 
 def _spans(tensors):
@@ -799,7 +813,7 @@ def grad_norm(tensors, ws: torch.Tensor, norm: Optional[torch.Tensor] = None, st
     synchronisation).  ws from new_grad_workspace."""
     tensors = list(tensors)
     norm = _norm_out(norm, ws)
-    arr = _tensor_list(tensors, "tensors", ws.device)
+    arr, _ = _tensor_list(tensors, "tensors", ws.device)
     with _device_of(ws.device):
         _check(_lib().moe_grad_norm(arr, len(tensors), _ptr(norm), _ptr(ws), ws.numel(), _stream_of(ws.device, stream)),
                "moe_grad_norm")
@@ -812,17 +826,17 @@ def clip_grads(tensors, max_norm: float, ws: torch.Tensor, out=None, norm: Optio
     sizes and types), and returns the norm before clipping, an fp32 scalar on the device (no synchronisation)."""
     tensors = list(tensors)
     norm = _norm_out(norm, ws)
-    arr = _tensor_list(tensors, "tensors", ws.device)
-    _no_overlap(_spans(tensors), "tensors")
+    arr, spans = _tensor_list(tensors, "tensors", ws.device)
     oarr = None
-    if out is not None:
+    if out is None:
+        _no_overlap(spans, "tensors")
+    else:
         out = list(out)
-        oarr = _tensor_list(out, "out", ws.device)
+        oarr, ospans = _tensor_list(out, "out", ws.device)
         if len(out) != len(tensors) or any(o.shape != t.shape or o.dtype != t.dtype for o, t in zip(out, tensors)):
             raise ValueError("out must hold a tensor of the same shape and type for each gradient")
-        mine = {i: s[:2] for *s, i in _spans(tensors)}
-        _no_overlap([s for s in _spans(out) if mine[s[2]] != s[:2]] + _spans(tensors), "gradients and out")
-        _no_overlap(_spans(out), "out")
+        # an output may be its gradient itself, and overlaps nothing else
+        _no_overlap(spans + [o for o, t in zip(ospans, spans) if o[:2] != t[:2]], "gradients or out")
     with _device_of(ws.device):
         _check(_lib().moe_clip_grads(arr, oarr, len(tensors), float(max_norm), _ptr(norm), _ptr(ws), ws.numel(),
                                      _stream_of(ws.device, stream)), "moe_clip_grads")
