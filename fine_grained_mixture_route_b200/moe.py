@@ -230,8 +230,9 @@ def _need_stack(w: Optional[Dict], name: str, shape: MoeShape, shared: bool, dev
                       ("b1", E * I, dt), ("b3", E * I, dt), ("b2", E * d, dt),
                       ("s1", E * I, torch.float32), ("s3", E * I, torch.float32), ("s2", E * d, torch.float32)):
         t = w.get(k)
-        if t is not None:
-            _need(t, f"{name}.{k}", n, kdt, device)
+        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype == kdt and t.is_contiguous() and t.numel() >= n
+                                  and (device is None or t.device == device)):
+            _need(t, f"{name}.{k}", n, kdt, device)             # says what is wrong
     if w.get("sf13") is not None:
         _need(w["sf13"], f"{name}.sf13", mx_scale_bytes(MX_UP, E, I, d), torch.uint8, device)
     if w.get("sf2") is not None:
@@ -649,7 +650,7 @@ def layer_forward_few(shape: MoeShape, x, centroids, routed: Dict, shared: Optio
 # ----------------------------------------------------------------------------- around the layer
 def _stream_of(dev: torch.device, stream=None):
     """The given stream, else the current stream of the tensors' device (which need not be the current device)."""
-    return ctypes.c_void_p((torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream)
+    return (torch.cuda.current_stream(dev.index) if stream is None else stream).cuda_stream
 
 
 _SAME_DEVICE = contextlib.nullcontext()
@@ -707,7 +708,7 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: 
     _on_cuda(dev)
     for k, spec in want.items():
         if spec is not None and o[k] is None:
-            o[k] = torch.empty(spec[0], dtype=spec[1], device=dev)
+            o[k] = torch.empty_like(x) if spec[0] == (rows, d) and spec[1] == dt else x.new_empty(spec[0], dtype=spec[1])
     with _device_of(dev):
         _check(_lib().moe_rmsnorm(MOE_BF16 if dt == torch.bfloat16 else MOE_F32, rows, d, _ptr(x), _ptr(residual),
                                   _ptr(weight), eps, _ptr(o["sum"]), _ptr(o["y"]), fmt, _ptr(o["codes"]),
@@ -762,30 +763,27 @@ def new_grad_workspace(device="cuda") -> torch.Tensor:
     return ws
 
 
+_GRAD_TYPES = {torch.bfloat16: (MOE_BF16, 2), torch.float32: (MOE_F32, 4)}   # moe_dtype_t, bytes
+
+
 def _tensor_list(tensors, name: str, device: torch.device):
     """(descriptors for the C entry points, [(first byte, end, index)] of the tensors that hold elements)."""
-    flat, spans = array.array("q"), []                          # moe_tensor_t: pointer, int64, int32 and padding
+    flat, spans = [], []                                        # moe_tensor_t: pointer, int64, int32 and padding
     for i, t in enumerate(tensors):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}[{i}] must be a torch.Tensor")
-        dt = t.dtype
-        if dt != torch.bfloat16 and dt != torch.float32:
-            raise ValueError(f"{name}[{i}] has dtype {dt}; bfloat16 or float32 is needed")
+        kind = _GRAD_TYPES.get(t.dtype)
+        if kind is None:
+            raise ValueError(f"{name}[{i}] has dtype {t.dtype}; bfloat16 or float32 is needed")
         if not t.is_contiguous():
             raise ValueError(f"{name}[{i}] must be contiguous")
         if t.device != device:
             raise ValueError(f"{name}[{i}] is on {t.device}; the workspace is on {device}")
         p, n = t.data_ptr(), t.numel()
-        if dt == torch.bfloat16:
-            flat.extend((p, n, MOE_BF16))
-            end = p + 2 * n
-        else:
-            flat.extend((p, n, MOE_F32))
-            end = p + 4 * n
+        flat += (p, n, kind[0])
         if n:
-            spans.append((p, end, i))
-    if not flat:
-        flat.extend((0, 0, 0))
+            spans.append((p, p + n * kind[1], i))
+    flat = array.array("q", flat or (0, 0, 0))
     return (MoeTensor * (len(flat) // 3)).from_buffer(flat), spans
 
 
