@@ -1325,6 +1325,7 @@ cudaError_t launch(Params& p, int grid, cudaStream_t st) {
     int n = (SMEM_LIMIT - rest) / p.stage;
     n = n > MAX_STAGES ? MAX_STAGES : n;
     p.nst = n * rows > RING_BYTES ? RING_BYTES / rows : n;
+    if (p.nst < 2) return cudaErrorInvalidValue;                // a consumer holds one stage while it waits for the next
     const Smem L(p.nst * p.stage, R * NT, p.T, p.E, p.k);
     auto kern = few_kernel<FR, NT, R>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);

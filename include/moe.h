@@ -544,7 +544,8 @@ typedef struct {
  * overlap the gradients of other entries.  Squares below fp32's range or above it are taken in 64 bits.
  * A norm of infinity gives coef 0 (infinite elements become NaN), a NaN norm gives NaN gradients.
  * max_norm must not be negative or NaN (infinity: no clipping).  No tensor may be listed twice.
- * ws: moe_grad_workspace_bytes() bytes, cleared once by moe_ws_init; sums in fixed order.
+ * ws: moe_grad_workspace_bytes() bytes, cleared once by moe_ws_init; calls that share one must not overlap.
+ * Sums in fixed order.
  */
 size_t moe_grad_workspace_bytes(void);
 moe_status_t moe_grad_norm(const moe_tensor_t* grads, int32_t n, float* norm, void* ws, size_t ws_bytes,

@@ -167,3 +167,61 @@ def test_few_binding_refuses_before_any_call():
                      (dict(routed=dict(L["routed"], w2=L["routed"]["w2"].float())), "routed.w2")):
         with pytest.raises(ValueError, match=what):
             call(**kw)
+
+
+# ------------------------------------------------------------------------------ the layer on rows in 8 bits
+def _q8_args(fmt="e4m3", T=4, d=64, E=4, I=32):
+    s = {k: torch.zeros(v, dtype=torch.uint8) for k, v in (("w1", (E, I, d)), ("w3", (E, I, d)), ("w2", (E, d, I)))}
+    if fmt == "e4m3":
+        s.update(s1=torch.zeros(E, I), s3=torch.zeros(E, I), s2=torch.zeros(E, d))
+    else:
+        s.update(sf13=torch.zeros(moe.mx_scale_bytes(moe.MX_UP, E, I, d), dtype=torch.uint8),
+                 sf2=torch.zeros(moe.mx_scale_bytes(moe.MX_DOWN, E, d, I), dtype=torch.uint8))
+    x, c = _m(T, d), _m(E, d)
+    shape = moe.shape_of(x, c, s, 2, None)
+    scale = torch.zeros(T) if fmt == "e4m3" else torch.zeros((T, -(-d // 32)), dtype=torch.uint8)
+    return dict(shape=shape, x=x, x_codes=torch.zeros((T, d), dtype=torch.uint8), x_scale=scale, centroids=c, routed=s,
+                shared=None, ws=torch.zeros(16, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "mxfp8"])
+def test_quantized_layer_refuses_before_any_call(fmt):
+    a = _q8_args(fmt)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.layer_forward_quantized(**a)
+    for bad, what in ((dict(x_codes=None), "x_codes"), (dict(x_scale=None), "x_scale"),
+                      (dict(x_codes=torch.zeros((4, 63), dtype=torch.uint8)), "x_codes holds"),
+                      (dict(x_codes=_m(4, 64)), "x_codes has dtype"), (dict(x_scale=a["x_scale"][:3]), "x_scale holds"),
+                      (dict(x_scale=torch.zeros((4, 2), dtype=torch.int8)), "x_scale has dtype"),
+                      (dict(ws=torch.zeros(4)), "ws has dtype")):
+        with pytest.raises((ValueError, TypeError), match=what):
+            moe.layer_forward_quantized(**{**a, **bad})
+
+
+def test_quantized_layer_needs_8_bit_experts():
+    a = _q8_args()
+    E, I, d = a["routed"]["w1"].shape
+    native = {"w1": torch.zeros((E, I, d), dtype=BF), "w3": torch.zeros((E, I, d), dtype=BF), "w2": torch.zeros((E, d, I), dtype=BF)}
+    shape = moe.shape_of(a["x"], a["centroids"], native, 2, None)
+    with pytest.raises(ValueError, match="8-bit"):
+        moe.layer_forward_quantized(**{**a, "shape": shape, "routed": native})
+
+
+def test_quantized_layer_c_entry_point_returns_errors():
+    lib, p, odd = moe.lib_handle(), ctypes.c_void_p(1 << 40), ctypes.c_void_p((1 << 40) + 8)      # never dereferenced
+
+    def call(fmt=moe.FMT_E4M3, x=p, codes=p, scales=p, ws=p, T=4):
+        sh = moe.make_shape(T, 64, 4, 32, 2, routed_fmt=fmt, has_bias=False)
+        w = moe.MoeWeights(w1=p, w3=p, w2=p)
+        if fmt == moe.FMT_E4M3:
+            w.s1 = w.s3 = w.s2 = p
+        elif fmt == moe.FMT_MXFP8:
+            w.sf13 = w.sf2 = p
+        return lib.moe_layer_forward_quantized(ctypes.byref(sh), x, codes, scales, p, None, ctypes.byref(w), None, p, None, None,
+                                               None, ws, 1 << 30, None)
+
+    assert call(T=0, x=None, codes=None, scales=None) == moe.MOE_OK
+    for kw in (dict(codes=None), dict(scales=None), dict(codes=odd), dict(x=None), dict(scales=ctypes.c_void_p((1 << 40) + 2))):
+        assert call(**kw) == moe.MOE_ERR_INVALID_ARG, kw
+    assert call(fmt=moe.FMT_NATIVE) == moe.MOE_ERR_UNSUPPORTED
+    assert call(ws=None) == moe.MOE_ERR_WORKSPACE
