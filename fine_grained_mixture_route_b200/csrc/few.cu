@@ -166,7 +166,11 @@ __device__ __forceinline__ float f16_scale(float m) {
     return __uint_as_float((uint32_t)((14 - e > 126 ? 126 : 14 - e) + 127) << 23);
 }
 
-__device__ __forceinline__ float scale_of_byte(uint32_t b) { return __uint_as_float(b ? b << 23 : 0x00400000u); }
+// 2^(b - 127) of the two low bytes of w (255: NaN), by way of bf16, which holds them all.
+__device__ __forceinline__ float2 scales_of_bytes(uint32_t w) {
+    const __nv_bfloat162_raw r = __nv_cvt_e8m0x2_to_bf162raw((__nv_fp8x2_storage_t)w);
+    return make_float2(__uint_as_float((uint32_t)r.x << 16), __uint_as_float((uint32_t)r.y << 16));
+}
 
 // A grid barrier is a count of arrivals, G per round, that only grows: round_end is the count that completes the
 // round in which it stands at `v`.
@@ -254,6 +258,13 @@ struct Frag {
 
     // acc += weights x activations
     __device__ __forceinline__ void multiply(float (&acc)[R][NT * 4], uint32_t mask) const {
+        float2 f[R][2];
+        if (F == W_MX) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) f[i][h] = scales_of_bytes(sf[i][h]);
+        }
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
 #pragma unroll
@@ -286,8 +297,7 @@ struct Frag {
                             mma_f16(to, a0.z, a1.z, a0.w, a1.w, v.z, v.w);
                         }
                     }
-                    const float f0 = F == W_MX ? scale_of_byte((sf[i][0] >> (8 * s)) & 0xFFu) : 1.f;
-                    const float f1 = F == W_MX ? scale_of_byte((sf[i][1] >> (8 * s)) & 0xFFu) : 1.f;
+                    const float f0 = F != W_MX ? 1.f : s ? f[i][0].y : f[i][0].x, f1 = F != W_MX ? 1.f : s ? f[i][1].y : f[i][1].x;
 #pragma unroll
                     for (int j = 0; j < 4 && (F == W_MX || (HL > 1 && F != W_BF16)); ++j) {
                         const float v = (F == W_MX ? t[0][j] : 0.f) + (HL > 1 ? t[HL - 1][j] : 0.f);

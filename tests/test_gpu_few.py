@@ -184,6 +184,19 @@ def test_fp8_rows_of_any_size(fmt, size):
     _check(L, _run(L), tiny=2.0 ** -118)
 
 
+def test_block_scales_of_the_smallest_byte():
+    # w2 near 2^-121: every run's scale is 2^-127 (byte 0).  Results lie near bf16's smallest normal number, 2^-126,
+    # below which its step is 2^-133: half of that on top
+    L = _case(T=3, d=272, E=6, I=48, k=2, bias=False)
+    L["routed"]["w2"] *= 2.0 ** -118
+    L["routed"] = quant.quantize_stack(L["routed"], "mxfp8")
+    sf2 = L["routed"]["sf2"]
+    assert (sf2 == 0).any() and ((sf2 == 0) | (sf2 == 127)).all()
+    o = _run(L)
+    assert (o["out"] != 0).any()
+    _check(L, o, tiny=2.0 ** -134)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "mxfp8"])
 def test_fp8_infinite_and_nan_inputs_stay_in_their_token(fmt):
     L = _case(T=5, d=272, E=8, I=48, k=3, fmt=fmt, bias=False)
