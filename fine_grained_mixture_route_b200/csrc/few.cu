@@ -98,6 +98,10 @@ struct Params {
     bool bias;
 };
 
+// Buffers of a unit's fragments: two that alternate save a barrier a unit; with 16 tokens on two row tiles one
+// leaves room for a third stage.
+__host__ __device__ constexpr int red_buffers(int frags) { return frags > 2 ? 1 : 2; }
+
 // Dynamic shared memory, in bytes from its start.
 constexpr int SPARE = ROUTE_WARPS * 4;                          // groups of 8 lanes that rank tokens
 struct Smem {
@@ -109,7 +113,7 @@ struct Smem {
         ring = take(ring_bytes);
         bars = take((2 * MAX_STAGES + 3) * 8);
         turns = take(3 * 8);
-        red = take(2 * CONS_WARPS * frags * 32 * 16);
+        red = take(red_buffers(frags) * CONS_WARPS * frags * 32 * 16);
         mask = take(E * 4);
         base = take(E * 4);
         ge = take(groups * 4);
@@ -408,7 +412,7 @@ __device__ __forceinline__ void unit_f32(float (&acc)[NT * 8], Me& me, int K, ui
 
 // The 8 warps' fragments of a unit to shared memory.  Fragment f = row tile * NT + group of 8 tokens; after the
 // barrier one warp adds up a fragment: c[0], c[1]: weight row lane / 4 of the tile, tokens 2 (lane % 4) and + 1;
-// c[2], c[3]: row lane / 4 + 8.  The two buffers alternate, so one barrier per unit is enough.
+// c[2], c[3]: row lane / 4 + 8.  Two buffers alternate, so that one barrier per unit is enough.
 template <int NT, int R>
 __device__ __forceinline__ void put_frag(float4* red, const float (&acc)[R][NT * 4], const Me& me) {
 #pragma unroll
@@ -989,6 +993,11 @@ struct Kernel {
         return f < FRAGS ? f : -1;
     }
 
+    // One buffer: the last unit's fragments have been read.
+    __device__ __forceinline__ void before_put() const {
+        if (red_buffers(FRAGS) == 1) named_sync(1, CONS);
+    }
+
     template <int F>
     __device__ __forceinline__ void up(Me& me, const Group& q, float4* red) {
         if constexpr (F == W_F32) {
@@ -996,6 +1005,7 @@ struct Kernel {
 #pragma unroll
             for (int n = 0; n < NT * 8; ++n) acc[n] = 0.f;
             unit_f32<NT>(acc, me, p.d, q.mask);
+            before_put();
             put_f32<NT>(red, acc, me);
         } else {
             float acc[R][NT * 4];
@@ -1004,6 +1014,7 @@ struct Kernel {
 #pragma unroll
                 for (int j = 0; j < NT * 4; ++j) acc[i][j] = 0.f;
             unit_mma<FR, F, NT, 1, R>(acc, me, Stage<FR, R>::scales(p.T), p.d, q.mask);
+            before_put();
             put_frag<NT, R>(red, acc, me);
         }
     }
@@ -1204,7 +1215,7 @@ struct Kernel {
         if (threadIdx.x == 0) grid_arrive(p.bar);
 
         int turn = 0;
-        auto buffer = [&] { return red0 + (turn & 1) * CONS_WARPS * FRAGS * 32; };
+        auto buffer = [&] { return red0 + (turn & (red_buffers(FRAGS) - 1)) * CONS_WARPS * FRAGS * 32; };
         const int su = shared_units();
         int units = su, met = 0;
         bool routed = false;
@@ -1268,6 +1279,7 @@ struct Kernel {
                 if (FR != FS && !q.shared) down<FR>(acc, me, q, cb);
                 else down<FS>(acc, me, q, cb);
             }
+            before_put();
             if constexpr (FR == W_F32) put_f32<NT>(buffer(), acc[0], me);
             else put_frag<NT, R>(buffer(), acc, me);
             named_sync(1, CONS);
