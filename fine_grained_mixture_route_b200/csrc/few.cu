@@ -7,7 +7,7 @@
 //   router scores (consumers) | shared experts' w1, w3 already arrive, they do not depend on the picks
 //   -> all blocks have written their scores: every block ranks all tokens itself (router warps), while its
 //      consumers work on the shared experts
-//   -> picked experts' w1, w3
+//   -> picked experts' w1, w3; the block's gates, ranked after the picks, are waited for before h and before b2
 //   -> all blocks have written h: w2, whose first stages arrived while the block waited.
 //
 // Work is cut into units of 32 weight rows (fp32: 16) over the full contraction: in each row tile of 16, 8 rows of
@@ -1242,6 +1242,8 @@ struct Kernel {
             if (f >= 0) finish_up(q, r, fin, take_frag<FRAGS>(buffer(), f, me.lane), f % NT, me.lane);
             ++turn;
         }
+        // add_b2 reads the block's own gates, also in a block that had no routed unit to wait for them
+        mbar_wait(gate_bar(), 0, abort_flag(), p.err);
         named_sync(1, CONS);                                    // the block's h is written
         if (threadIdx.x == 0) {
             grid_arrive(p.bar + 1);

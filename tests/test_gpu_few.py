@@ -272,3 +272,21 @@ def test_no_tokens():
     shape = moe.shape_of(x, L["centroids"], L["routed"], 2, None)
     out = moe.layer_forward_few(shape, x, L["centroids"], L["routed"], None, moe.new_few_workspace(shape))
     assert out.shape == (0, 64)
+
+
+@pytest.mark.parametrize("kw", [dict(T=16, d=1024, E=1024, I=8, k=1), dict(T=16, d=2048, E=600, I=16, k=2, Ks=1, Is=8),
+                                dict(T=1, d=1280, E=64, I=320, k=7, Ks=1)],
+                         ids=lambda s: "-".join(f"{k}{v}" for k, v in s.items()))
+def test_gates_of_blocks_without_a_routed_unit(kw):
+    # fewer units of the up-projection than SMs, and many gates to compute: blocks that had none of them add b2 with
+    # gates that nothing else made them wait for.  b2 dominates the result; other calls before each repeat leave other
+    # gates in shared memory
+    L = _case(**kw)
+    L["routed"]["b2"].normal_(0.0, 30.0, generator=torch.Generator(device="cuda").manual_seed(3))
+    other = _case(**dict(kw, T=max(1, kw["T"] // 2)), seed=8)
+    o = _run(L)
+    _check(L, o)
+    first = o["out"].clone()
+    for _ in range(20):
+        _run(other)
+        assert torch.equal(_run(L)["out"], first)
