@@ -26,13 +26,14 @@
 // accumulators.  tcgen05's smallest tile is 64 or 128 weight rows, too coarse to spread a few experts evenly
 // over 148 SMs, and takes 8-bit weights only against 8-bit activations; here the bound is HBM, the tensor
 // pipe idles.  Scales are applied to fp32 sums (block scales: each run of 32 has its own sum).  Activations are
-// not quantised: x is bf16 as given, and h is kept as the sum of two bf16 numbers (16 significant bits).
+// not quantised: x is bf16 as given, and h is fp32, which the consumers cut into three bf16 parts of 8 bits each as they
+// load it (exact): it costs no rounding, and no more bytes of the ring than two parts would.
 // 8-bit codes become fp16, exactly and in one instruction a pair (bf16 takes four, and the conversions then
 // bound the kernel: 185 us instead of 165 for w1, w3 of 22 block-scaled experts of 2048 x 7168).  Their
 // activations are therefore fp16 too, each row times a power of two that brings its largest finite value into
 // [2^14, 2^15): x in one number (its 8 bits are kept down to 2^-28 of that, and 2^-40 of it is the largest error), h in
-// two (22 bits), for which the rows' largest values have to be known: one grid barrier more, behind which the
-// rows are converted, while the first weights of w2 arrive.
+// two (22 bits of its fp32 value), for which the rows' largest values have to be known: one grid barrier more, behind
+// which the rows are converted, while the first weights of w2 arrive.
 // A thread's k-columns need only be the same for both operands, so every fragment is a plain 16- or 8-byte
 // load, without ldmatrix.
 // fp32 layers take the same route with FFMA.
@@ -68,13 +69,19 @@ struct Fmt {
     static constexpr int PITCH = ROWB + (esz == 1 ? 32 : 64);
     static constexpr int PER_WARP = KS / CONS_WARPS;
 };
-constexpr int ACT = 1024 + 64;                                  // 512 bf16 or 256 fp32 columns
+constexpr int ACT = 1024 + 64;                                  // a row of x: 512 columns of 16 bits or 256 of 32
+// A row of h: 4 bytes a column, fp32 or 8 fp16 high parts and their 8 low parts in turn.  A thread of the MMAs reads 32
+// bytes at 4 places 32 bytes apart and 8 rows: 16 bytes more than a multiple of 128 keep those apart.
+template <int FR, int F>
+constexpr int hrow() { return FR == W_F32 ? ACT : Fmt<FR, F>::KS * 4 + 16; }
 template <int FR, int R>
 struct Stage {
-    static constexpr int HL = FR == W_F32 ? 1 : 2;              // parts of an activation row
+    static constexpr int act = hrow<FR, FR>() > ACT ? hrow<FR, FR>() : ACT;      // of a token, at most
     static constexpr int acts = 16 * R * (Fmt<FR, FR>::ROWB + 64);
-    static __host__ __device__ int scales(int T) { return acts + T * HL * ACT; }
-    static __host__ __device__ int bytes(int T) { return scales(T) + (FR == W_MX ? 16 * R * 16 : 0); }
+    static __host__ __device__ int scales(int T) { return acts + T * act; }
+    // Weight rows at a multiple of 128 bytes in every stage: 16 bytes off, the copies are slower (one token on 256 experts
+    // of 2048 x 7168: 142 us instead of 131)
+    static __host__ __device__ int bytes(int T) { return (scales(T) + (FR == W_MX ? 16 * R * 16 : 0) + 127) / 128 * 128; }
 };
 
 struct Params {
@@ -86,7 +93,7 @@ struct Params {
     float* gate;
     int32_t* counts;
     float* logits;                                              // [T][E]
-    void* h;                                                    // bf16 [rows][2][Hs] (high, low part), fp32 [rows][Hs]
+    float* h;                                                   // [rows][Hs]; 8-bit experts' rows: see convert_h
     __half* x16;                                                // 8-bit experts: [T][d], row t times 1 / xf[t]
     float* xf;
     unsigned* hmax;                                             // their rows' largest finite |h|, as bits
@@ -220,9 +227,32 @@ struct Ring {
 
 __device__ __forceinline__ uint4 lds128(const char* a) { return *reinterpret_cast<const uint4*>(a); }
 
+// With an infinite number or NaN among its columns a first part's sum is not finite, and stands alone.
+__device__ __forceinline__ float add_parts(float first, float others) { return fabsf(first) < INFINITY ? first + others : first; }
+
+// 8 fp32 numbers as the sum of three bf16 ones, exactly: each part is the upper half of what is left, its top 8 bits.
+// Of an infinite number or NaN the first part is one too, and the others mean nothing.
+__device__ __forceinline__ void bf16_parts(const uint4 (&v)[2], uint4 (&part)[3]) {
+    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+    uint32_t o[3][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a = w[2 * i], b = w[2 * i + 1];
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            o[q][i] = __byte_perm(a, b, 0x7632);
+            if (q == 2) break;
+            a = __float_as_uint(__uint_as_float(a) - __uint_as_float(a & 0xFFFF0000u));
+            b = __float_as_uint(__uint_as_float(b) - __uint_as_float(b & 0xFFFF0000u));
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 3; ++q) part[q] = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
+}
+
 // A thread's fragments of a stage: 16 R weight rows and up to 8 NT tokens over the warp's columns, wk from the
 // stage's start and kb < K of all.  act[nt]: where the thread's token's row is in the stage (0: the token is not
-// among the unit's); HL = 2: its low part follows ACT bytes on.  Columns past K hold an earlier stage's bytes:
+// among the unit's); HL = 1: a row of x, HL = 2: one of h.  Columns past K hold an earlier stage's bytes:
 // both operands are zeroed.  sf: the scale bytes of the warp's 2 runs.
 template <int FR, int F, int NT, int HL, int R>
 struct Frag {
@@ -244,7 +274,7 @@ struct Frag {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int q = 0; q < HL; ++q)
-                    b[s][nt][q] = in && act[nt] ? *reinterpret_cast<const uint4*>(stage + act[nt] + q * ACT + k * 2) : make_uint4(0, 0, 0, 0);
+                    b[s][nt][q] = in && act[nt] ? *reinterpret_cast<const uint4*>(stage + act[nt] + k * 2 * HL + q * 16) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -260,55 +290,70 @@ struct Frag {
         }
     }
 
-    // acc += weights x activations
+    // acc += weights x activations.  The tensor cores cut off what they add to a large sum instead of rounding it, always
+    // towards zero: a stage (8-bit weights: a step of 32 columns, in which block scales are constant) has its own short
+    // sum, and those are added in fp32.
     __device__ __forceinline__ void multiply(float (&acc)[R][NT * 4], uint32_t mask) const {
-        float2 f[R][2];
-        if (F == W_MX) {
+        if constexpr (F == W_BF16) {
 #pragma unroll
-            for (int i = 0; i < R; ++i)
+            for (int nt = 0; nt < NT; ++nt) {
+                if (NT > 1 && ((mask >> (8 * nt)) & 0xFFu) == 0u) continue;
+                constexpr int PARTS = HL > 1 ? 3 : 1;
+                float t[PARTS][R][4] = {};                      // one for each part: short chains of products
 #pragma unroll
-                for (int h = 0; h < 2; ++h) f[i][h] = scales_of_bytes(sf[i][h]);
-        }
+                for (int s = 0; s < STEPS; ++s) {
+                    uint4 v[PARTS];
+                    if constexpr (HL > 1) bf16_parts(b[s][nt], v);
+                    else v[0] = b[s][nt][0];
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s)
+                    for (int q = 0; q < PARTS; ++q)
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                uint4 a0, a1;
-                if constexpr (F == W_BF16) {
-                    a0 = a[s][i][0];
-                    a1 = a[s][i][1];
-                } else {
+                        for (int i = 0; i < R; ++i) {
+                            const uint4 &a0 = a[s][i][0], &a1 = a[s][i][1];
+                            mma_bf16(t[q][i], a0.x, a1.x, a0.y, a1.y, v[q].x, v[q].y);
+                            mma_bf16(t[q][i], a0.z, a1.z, a0.w, a1.w, v[q].z, v[q].w);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        acc[i][nt * 4 + j] += HL > 1 ? add_parts(t[0][i][j], t[PARTS > 1][i][j] + t[PARTS - 1][i][j]) : t[0][i][j];
+                    }
+            }
+        } else {
+            float2 f[R][2];
+            if (F == W_MX) {
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) f[i][h] = scales_of_bytes(sf[i][h]);
+            }
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
                     const uint2 l0 = f16_of_codes(a[s][i][0].x), h0 = f16_of_codes(a[s][i][0].y);
                     const uint2 l1 = f16_of_codes(a[s][i][1].x), h1 = f16_of_codes(a[s][i][1].y);
-                    a0 = make_uint4(l0.x, l0.y, h0.x, h0.y);
-                    a1 = make_uint4(l1.x, l1.y, h1.x, h1.y);
-                }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (NT > 1 && ((mask >> (8 * nt)) & 0xFFu) == 0u) continue;
-                    // Block scales: a run's own sum, scaled in fp32.  8-bit weights: the low parts' sums too, half the
-                    // chain of products.
-                    float t[HL][4] = {};
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (NT > 1 && ((mask >> (8 * nt)) & 0xFFu) == 0u) continue;
+                        float t[HL][4] = {};                    // high and low parts apart: half the chain of products
 #pragma unroll
-                    for (int q = 0; q < HL; ++q) {
-                        const uint4& v = b[s][nt][q];
-                        float* to = F == W_MX || (q > 0 && F != W_BF16) ? t[q] : acc[i] + nt * 4;
-                        if (F == W_BF16) {
-                            mma_bf16(to, a0.x, a1.x, a0.y, a1.y, v.x, v.y);
-                            mma_bf16(to, a0.z, a1.z, a0.w, a1.w, v.z, v.w);
-                        } else {
-                            mma_f16(to, a0.x, a1.x, a0.y, a1.y, v.x, v.y);
-                            mma_f16(to, a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+                        for (int q = 0; q < HL; ++q) {
+                            const uint4& v = b[s][nt][q];
+                            mma_f16(t[q], l0.x, l1.x, l0.y, l1.y, v.x, v.y);
+                            mma_f16(t[q], h0.x, h1.x, h0.y, h1.y, v.z, v.w);
+                        }
+                        const float f0 = F != W_MX ? 1.f : s ? f[i][0].y : f[i][0].x, f1 = F != W_MX ? 1.f : s ? f[i][1].y : f[i][1].x;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float v = HL > 1 ? t[0][j] + t[HL - 1][j] : t[0][j];
+                            acc[i][nt * 4 + j] = fmaf(v, j < 2 ? f0 : f1, acc[i][nt * 4 + j]);
                         }
                     }
-                    const float f0 = F != W_MX ? 1.f : s ? f[i][0].y : f[i][0].x, f1 = F != W_MX ? 1.f : s ? f[i][1].y : f[i][1].x;
-#pragma unroll
-                    for (int j = 0; j < 4 && (F == W_MX || (HL > 1 && F != W_BF16)); ++j) {
-                        const float v = (F == W_MX ? t[0][j] : 0.f) + (HL > 1 ? t[HL - 1][j] : 0.f);
-                        acc[i][nt * 4 + j] = fmaf(v, j < 2 ? f0 : f1, acc[i][nt * 4 + j]);
-                    }
                 }
-            }
+        }
     }
 };
 
@@ -340,7 +385,7 @@ __device__ __forceinline__ void unit_mma(float (&acc)[R][NT * 4], Me& me, int sf
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int n = nt * 8 + (me.lane >> 2);
-        act[nt] = (mask >> n) & 1u ? Stage<FR, R>::acts + __popc(mask & ((1u << n) - 1u)) * HL * ACT : 0;
+        act[nt] = (mask >> n) & 1u ? Stage<FR, R>::acts + __popc(mask & ((1u << n) - 1u)) * (HL > 1 ? hrow<FR, F>() : ACT) : 0;
     }
     // With 8-bit weights the latencies of a stage (shared memory, conversions, a chain of products), two warps a
     // scheduler, take longer than its bytes: where the registers allow it (one part an activation), a stage's
@@ -377,6 +422,80 @@ __device__ __forceinline__ void unit_mma(float (&acc)[R][NT * 4], Me& me, int sf
             if (k0 >= K) break;
         }
     }
+}
+
+// A unit of the down-projection with 16-bit weights and one or two tokens, as most units of routed experts have: the parts
+// of h take the free columns of the products, which makes a third of them (16 tokens on 64 experts of 1408 x 2048: 191 us
+// instead of 202).  Column 4 j + q is part q of the unit's token j.  t: as unit_mma's.  Layers with 8-bit experts have only
+// their shared ones here, and the registers are worth more to the others (four tokens, e4m3: 264 us instead of 256).
+template <int FR, int NT, int R>
+__device__ __forceinline__ void unit_parts(float (&t)[R][NT * 4], Me& me, int K, uint32_t mask) {
+    using L = Fmt<FR, W_BF16>;
+    constexpr int STEPS = L::PER_WARP / 32;
+    const int wk = me.warp * L::PER_WARP, g = me.lane >> 2, c = (me.lane & 3) * 8, j = g >> 2, q = g & 3;
+    const bool mine = j < __popc(mask) && q < 3;
+    const char* row = me.sm + g * L::PITCH;
+    const int act = Stage<FR, R>::acts + j * hrow<FR, W_BF16>();
+    const uint32_t m1 = q > 0 ? 0xFFFF0000u : 0u, m2 = q > 1 ? 0xFFFF0000u : 0u;    // what the parts before hold
+    float acc[R][4] = {};
+    for (int k0 = 0; k0 < K; k0 += L::KS) {
+        wait_full(me, me.ring);
+        if (k0 + wk < K) {
+            const int at = me.ring.slot * me.ring.stage;
+            uint4 a[STEPS][R][2], v[STEPS][2];
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int k = wk + s * 32 + c;
+                const bool in = k0 + k < K;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) v[s][h] = in && mine ? lds128(me.sm + at + act + k * 4 + h * 16) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) a[s][i][h] = in ? lds128(row + at + (i * 16 + h * 8) * L::PITCH + k * 2) : make_uint4(0, 0, 0, 0);
+            }
+            float sum[R][4] = {};
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                uint32_t w[8] = {v[s][0].x, v[s][0].y, v[s][0].z, v[s][0].w, v[s][1].x, v[s][1].y, v[s][1].z, v[s][1].w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float r = __uint_as_float(w[e]) - __uint_as_float(w[e] & m1);
+                    w[e] = __float_as_uint(r - __uint_as_float(__float_as_uint(r) & m2));
+                }
+                const uint32_t b0 = __byte_perm(w[0], w[1], 0x7632), b1 = __byte_perm(w[2], w[3], 0x7632);
+                const uint32_t b2 = __byte_perm(w[4], w[5], 0x7632), b3 = __byte_perm(w[6], w[7], 0x7632);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const uint4 &a0 = a[s][i][0], &a1 = a[s][i][1];
+                    mma_bf16(sum[i], a0.x, a1.x, a0.y, a1.y, b0, b1);
+                    mma_bf16(sum[i], a0.z, a1.z, a0.w, a1.w, b2, b3);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][e] += sum[i][e];
+        }
+        release(me);
+    }
+    // Columns 4 j, 4 j + 1 are in the lanes with lane % 4 = 2 j, column 4 j + 2 in the next ones
+    const int tok0 = __ffs(mask) - 1, tok1 = __ffs(mask & (mask - 1u)) - 1, quad = me.lane & ~3;
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float low = acc[i][2 * h + 1] + __shfl_down_sync(0xffffffffu, acc[i][2 * h], 1);
+            const float all = add_parts(acc[i][2 * h], low);
+            const float y0 = __shfl_sync(0xffffffffu, all, quad), y1 = __shfl_sync(0xffffffffu, all, quad + 2);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int tok = nt * 8 + (me.lane & 3) * 2 + e;
+                    t[i][nt * 4 + h * 2 + e] = tok == tok0 ? y0 : tok == tok1 ? y1 : 0.f;
+                }
+        }
 }
 
 // One unit of 16 rows in fp32: lane pairs share a row, each lane every other 16-byte piece of the warp's
@@ -598,9 +717,9 @@ struct Kernel {
         const char* row[8 * R];                                 // this lane's 16 bytes of the first stage
         int bytes, esz;                                         // of a weight row, of a weight
         const char* act;                                        // activations of the unit's first token, this lane's part
-        int act_row, act_low;                                   // bytes between tokens' rows, and to the low part (0: none)
+        int act_row;                                            // bytes between tokens' rows
         uint32_t mask;
-        bool by_token;                                          // rows of x: by token; of h: in order
+        bool down;                                              // rows of h, in order; else rows of x, by token
         const char* sf;                                         // this lane's row's scale word of the first 128 columns
         // row j of tile i: row i * tile + j of the matrix at `at`, of which `there` rows are left
         __device__ __forceinline__ void rows(const void* at, int tile, int there, int lane) {
@@ -634,25 +753,27 @@ struct Kernel {
         }
     }
     __device__ __forceinline__ void copy_acts(const Source& q, const Ring& ring, int c, int w, int lane) const {
-        const int up = q.esz == 1 ? 1 : 0, c0 = c << up, end = q.bytes << up;    // 8-bit weights have 16-bit activations
-        const bool in0 = c0 + lane * 16 < end, in1 = (Fmt<FR, FR>::ROWB << up) > 512 && c0 + 512 + lane * 16 < end;
-        uint32_t dst = ring.at() + Stage<FR, R>::acts + lane * 16 + w * ACT;
-        const char* a = q.act + c0;
-        auto copy = [&](const char* src) {
+        constexpr int ROWB = Fmt<FR, FR>::ROWB;
+        const uint32_t to = ring.at() + Stage<FR, R>::acts + lane * 16;
+        auto copy = [](uint32_t dst, const char* src, bool in0, bool in1) {
             if (in0) async_load<16>(dst, src);
             if (in1) async_load<16>(dst + 512, src + 512);
-            dst += 2 * ACT;
         };
-        if (q.act_low) {                                        // this warp: one part of all rows
-            a += w * q.act_low;
-            for (int n = __popc(q.mask); n > 0; --n, a += q.act_row) copy(a);
-        } else if (!q.by_token) {
-            a += w * q.act_row;
-            for (int n = __popc(q.mask) - w; n > 0; n -= 2, a += 2 * q.act_row) copy(a);
-        } else {
-            uint32_t m = w ? q.mask & (q.mask - 1u) : q.mask;
+        if (q.down) {                                           // this warp: one half (512 or 1024 bytes) of all rows
+            const int up = q.esz == 1 ? 2 : q.esz == 2 ? 1 : 0; // 4 bytes a column
+            const int half = (ROWB << up) / 2, c0 = (c << up) + w * half, end = q.bytes << up;
+            const int pitch = FR == W_F32 ? ACT : 2 * half + 16;               // hrow
+            const bool in0 = c0 + lane * 16 < end, in1 = half > 512 && c0 + 512 + lane * 16 < end;
+            uint32_t dst = to + w * half;
+            const char* a = q.act + c0;
+            for (int n = __popc(q.mask); n > 0; --n, a += q.act_row, dst += pitch) copy(dst, a, in0, in1);
+        } else {                                                // every other row
+            const int up = q.esz == 1 ? 1 : 0, c0 = c << up, end = q.bytes << up;    // 8-bit weights have 16-bit x
+            const bool in0 = c0 + lane * 16 < end, in1 = (ROWB << up) > 512 && c0 + 512 + lane * 16 < end;
+            uint32_t dst = to + w * ACT, m = w ? q.mask & (q.mask - 1u) : q.mask;
             while (m) {
-                copy(a + (size_t)(__ffs(m) - 1) * q.act_row);
+                copy(dst, q.act + c0 + (size_t)(__ffs(m) - 1) * q.act_row, in0, in1);
+                dst += 2 * ACT;
                 m &= m - 1u;
                 m &= m - 1u;
             }
@@ -669,8 +790,8 @@ struct Kernel {
         q.bytes = p.d * esz; q.esz = esz;
         q.rows(static_cast<const char*>(m) + ((size_t)g.e * I + r0) * q.bytes, 8, I - r0, lane);
         q.act = (Q8 && !g.shared ? reinterpret_cast<const char*>(p.x16) : static_cast<const char*>(p.x)) + lane * 16;
-        q.act_row = p.d * (int)sizeof(T); q.act_low = 0;
-        q.mask = g.mask; q.by_token = true; q.sf = nullptr;
+        q.act_row = p.d * (int)sizeof(T);
+        q.mask = g.mask; q.down = false; q.sf = nullptr;
         const int r = r0 + (lane >> 4) * 8 + (lane & 7);        // of the lane's row in the stage
         if (FR == W_MX && !g.shared && lane < DOWN && r < I)
             q.sf = reinterpret_cast<const char*>(p.R.sf13) + ((size_t)g.e * ceil_div(I, 128) + r / 128) * ceil_div(p.d, 128) * 1024 +
@@ -686,10 +807,9 @@ struct Kernel {
         Source q;
         q.bytes = I * esz; q.esz = esz;
         q.rows(static_cast<const char*>(m) + ((size_t)g.e * p.d + r0 + w * 8) * q.bytes, 16, p.d - r0 - w * 8, lane);
-        q.act_row = p.Hs * 4;                                   // two bf16 parts, or fp32
-        q.act_low = FR == W_F32 ? 0 : p.Hs * 2;
-        q.act = static_cast<const char*>(p.h) + (size_t)g.row * q.act_row + lane * 16;
-        q.mask = g.mask; q.by_token = false; q.sf = nullptr;
+        q.act_row = p.Hs * 4;
+        q.act = reinterpret_cast<const char*>(p.h) + (size_t)g.row * q.act_row + lane * 16;
+        q.mask = g.mask; q.down = true; q.sf = nullptr;
         const int r = r0 + lane;
         if (FR == W_MX && !g.shared && lane < DOWN && r < p.d)
             q.sf = reinterpret_cast<const char*>(p.R.sf2) + ((size_t)g.e * ceil_div(p.d, 256) + r / 256) * ceil_div(I, 128) * 1024 +
@@ -955,22 +1075,21 @@ struct Kernel {
         }
     }
 
-    // The rows of h of the 8-bit experts, in place: two bf16 parts -> two fp16 parts of h * f16_scale(largest).
+    // The rows of h of the 8-bit experts, in place: 8 fp32 numbers -> the two fp16 parts of h * f16_scale(largest), 8 high
+    // parts, then 8 low ones.
     __device__ void convert_h() {
         const int nv = p.I / 8, rows = h_rows();
         for (int i = blockIdx.x * CONS + threadIdx.x; i < rows * nv; i += G * CONS) {
             const int row = i / nv;
-            uint4* hi = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.h) + (size_t)row * 2 * p.Hs) + i % nv;
-            uint4* lo = hi + p.Hs / 8;
+            uint4* hi = reinterpret_cast<uint4*>(p.h + (size_t)row * p.Hs) + i % nv * 2;
+            uint4* lo = hi + 1;
             const float f = f16_scale(__uint_as_float(__ldcg(p.hmax + row)));
             const uint4 a = __ldcg(hi), b = __ldcg(lo);
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
             uint32_t ow[2][4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                // the parts' sum has 16 bits and is exact
-                const float v0 = (__uint_as_float(aw[q] << 16) + __uint_as_float(bw[q] << 16)) * f;
-                const float v1 = (__uint_as_float(aw[q] & 0xFFFF0000u) + __uint_as_float(bw[q] & 0xFFFF0000u)) * f;
+                const float v0 = __uint_as_float(w[2 * q]) * f, v1 = __uint_as_float(w[2 * q + 1]) * f;
                 const __half2 h = __floats2half2_rn(v0, v1);
                 const float2 g = __half22float2(h);
                 const float r0 = v0 - g.x, r1 = v1 - g.y;       // infinite or NaN: no low part
@@ -1065,15 +1184,7 @@ struct Kernel {
             }
             if (!mine) continue;
             const size_t row = q.row + __popc(q.mask & ((1u << tok) - 1u));
-            if (FR == W_F32) {
-                static_cast<float*>(p.h)[row * p.Hs + r] = h;
-            } else {
-                const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-                const float rest = h - __bfloat162float(hi);
-                __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.h) + row * 2 * p.Hs + r;
-                o[0] = hi;
-                o[p.Hs] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.f);
-            }
+            p.h[row * p.Hs + r] = h;
         }
     }
 
@@ -1151,7 +1262,8 @@ struct Kernel {
                     m[nt][j] = 0u;
                     if (F != W_BF16 && ((q.mask >> tok) & 1u)) m[nt][j] = __ldcg(p.hmax + row);
                 }
-            unit_mma<FR, F, NT, 2, R>(t, me, Stage<FR, R>::scales(p.T), K, q.mask);
+            if (FR == W_BF16 && __popc(q.mask) <= 2) unit_parts<FR, NT, R>(t, me, K, q.mask);
+            else unit_mma<FR, F, NT, 2, R>(t, me, Stage<FR, R>::scales(p.T), K, q.mask);
 #pragma unroll
             for (int j = 0; j < NT * 4; ++j) {
                 const int tok = j / 4 * 8 + (me.lane & 3) * 2 + (j & 1);
@@ -1332,7 +1444,7 @@ Layout few_layout(const Dims& D) {
     L.Hs = (widest + 7) / 8 * 8;
     size_t o = 256;
     L.logits = o; o += al256(T * D.E * 4);
-    L.h = o; o += al256(T * (D.k + D.Ks) * L.Hs * 4);           // two bf16 parts, or fp32
+    L.h = o; o += al256(T * (D.k + D.Ks) * L.Hs * 4);
     L.x16 = o; o += D.q8 ? al256(T * D.d * 2) : 0;
     L.xf = o; o += D.q8 ? al256(T * 4) : 0;
     L.hmax = o; o += D.q8 ? al256(T * D.k * 4) : 0;
@@ -1386,7 +1498,7 @@ cudaError_t launch_few(const Dims& D, const void* x, const void* cen, const floa
     p.x = x; p.cen = cen; p.rbias = rbias; p.R = R; p.Sh = Sh;
     p.out = out; p.idx = idx; p.gate = gate; p.counts = counts;
     p.logits = reinterpret_cast<float*>(w + L.logits);
-    p.h = w + L.h;
+    p.h = reinterpret_cast<float*>(w + L.h);
     p.x16 = reinterpret_cast<__half*>(w + L.x16);
     p.xf = reinterpret_cast<float*>(w + L.xf);
     p.hmax = reinterpret_cast<unsigned*>(w + L.hmax);

@@ -290,3 +290,51 @@ def test_gates_of_blocks_without_a_routed_unit(kw):
     for _ in range(20):
         _run(other)
         assert torch.equal(_run(L)["out"], first)
+
+
+@pytest.mark.parametrize("where,fmt", [("routed", None), ("routed", "e4m3"), ("routed", "mxfp8"), ("shared", None), ("shared", "e4m3")])
+@pytest.mark.parametrize("T,I", [(1, 16), (11, 1408)])
+def test_hidden_values_that_nearly_cancel(where, fmt, T, I):
+    # h0 = s (1 + 2^-18), h1 = s, w2 = (1, -1): the result is 2^-18 s, which hidden values of 16 bits lose whole.
+    # h in fp32, or in two fp16 parts of 22 bits: two of them are off by 2 (4 * 2^-24 + 2^-23) with the roundings of b's
+    # scales, and the two products' sum by 2 * 2^-23 if it truncates, in units of s: less than 2^-20
+    L = _case(T=T, d=256, E=1, I=I, k=1, Ks=1, bias=False)
+    for n in ("routed", "shared"):
+        for w in ("w1", "w3", "w2"):
+            L[n][w].zero_()
+    L["x"].zero_()
+    L["x"][:, 0], L["x"][:, 1] = 1.0, 2.0 ** -18
+    i, j = I - 13, I - 5                                        # within one product of 16 columns
+    w = L[where]
+    w["w1"][0, [i, j], 0] = 1.0
+    w["w3"][0, [i, j], 0] = 1.0
+    w["w3"][0, i, 1] = 1.0
+    w["w2"][0, :, i], w["w2"][0, :, j] = 1.0, -1.0
+    if fmt:
+        L["routed"] = quant.quantize_stack(L["routed"], fmt)
+    o = _run(L)
+    assert moe.check_device_error(o["ws"]) == 0
+    ref, _ = R.few_layer(L["x"], o["idx"], o["gate"], L["routed"], L["shared"], 1)
+    assert (ref > 0.7 * 2.0 ** -18).all()
+    assert ((o["out"].double() - ref).abs() <= 2.0 ** -8 * ref + 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3"])
+def test_infinite_hidden_values_stay_infinite(fmt):
+    # a hidden value beyond fp32's range times finite weights: infinite where the weight is not 0, and NaN where it is
+    L = _case(T=2, d=64, E=1, I=32, k=1, Ks=1, bias=False)
+    for n in ("routed", "shared"):
+        for w in ("w1", "w3", "w2"):
+            L[n][w].zero_()
+    L["x"][:] = 0
+    L["x"][0, 0], L["x"][1, 0] = 2.0 ** 100, 1.0
+    L["shared"]["w1"][0, 5, 0] = L["shared"]["w3"][0, 5, 0] = 1.0
+    L["shared"]["w2"][0, :, 5] = torch.linspace(-1, 1, 64, device="cuda")
+    L["shared"]["w2"][0, 9, 5] = 0.0
+    if fmt:
+        L["routed"] = quant.quantize_stack(L["routed"], fmt)
+    out = _run(L)["out"].float()
+    sign = torch.sign(L["shared"]["w2"][0, :, 5].float())
+    keep = torch.arange(64, device="cuda") != 9
+    assert torch.equal(out[0, keep], sign[keep] * float("inf")) and torch.isnan(out[0, 9])
+    assert torch.isfinite(out[1]).all() and (out[1, keep] != 0).all()
