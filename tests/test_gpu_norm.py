@@ -205,3 +205,38 @@ def test_captured_on_a_side_stream():
         torch.cuda.synchronize()
         assert all(torch.equal(out[k], want[k]) for k in want)
         assert torch.equal(dx, dwant[0]) and torch.equal(dw, dwant[1])
+
+
+@pytest.mark.parametrize("rows", [1, 700])
+def test_codes_between_two_steps_go_to_the_even_one(rows):
+    # a row whose mean square is 1 exactly, with the largest value 49: scale 49 / 448 = 7 / 64, and 7 n / 2^j over it is
+    # n * 2^(6 - j), with n odd and of 5 bits halfway between two codes.  Times the rounded reciprocal of 7 / 64 it is not
+    d = 8192
+    v = [49.0] + [s * 7 * n / 2.0 ** j for n in range(17, 32, 2) for j in (4, 5) for s in (1, -1)]
+    left = d - sum(t * t for t in v)
+    while left > 0:                                             # the rest: powers of two
+        t = 1.0
+        while t * t > left:
+            t /= 2
+        v.append(t)
+        left -= t * t
+    assert left == 0 and len(v) <= d
+    x = torch.tensor(v + [0.0] * (d - len(v)), device="cuda").bfloat16()
+    assert torch.equal(x.double().square().sum().cpu(), torch.tensor(float(d), dtype=torch.float64))
+    o = moe.rmsnorm(x.repeat(rows, 1), torch.ones(d, device="cuda", dtype=torch.bfloat16), eps=0.0, fmt=moe.FMT_E4M3)
+    assert (o["rstd"] == 1).all() and (o["scale"] == 7.0 / 64.0).all() and torch.equal(o["y"], x.repeat(rows, 1))
+    want = (x.double() / (7.0 / 64.0)).float().to(torch.float8_e4m3fn).view(torch.uint8)      # to the nearest, ties to even
+    assert torch.equal(o["codes"], want.repeat(rows, 1))
+    codes, scale = moe.quantize_rows_e4m3(o["y"], torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    assert torch.equal(codes, o["codes"]) and torch.equal(scale, o["scale"])
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -30, 2.0 ** 30])
+def test_codes_are_those_of_the_ieee_quotient(size):
+    # 33 million values over their rows' scales, from the rstd and scale that the kernel returns, in the order of its products
+    x = torch.randn(4096, 8192, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16() * size
+    w = (torch.randn(8192, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda") * (1 if size == 1 else 2.0 ** -70)).bfloat16()
+    o = moe.rmsnorm(x, w, eps=0.0, fmt=moe.FMT_E4M3)
+    v = x.float() * o["rstd"][:, None] * w.float()
+    assert torch.equal(o["y"], v.bfloat16())
+    assert torch.equal((v / o["scale"][:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8), o["codes"])
