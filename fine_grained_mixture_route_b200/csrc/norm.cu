@@ -56,26 +56,23 @@ struct Pack<float, 1> {
     __device__ __forceinline__ void zero() { r = 0.f; }
 };
 
-// Sum of a and maximum of b over the row's threads: a warp (WARP) or the block.
+// Sum or maximum of a over the row's threads: a warp (WARP) or the block.
 template <bool WARP, bool MAX>
-__device__ __forceinline__ void reduce_row(float& a, float& b, float2* sm) {
+__device__ __forceinline__ void reduce_row(float& a, float* sm) {
+    auto all = [&] {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        if (MAX) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-    }
+        for (int o = 16; o > 0; o >>= 1) {
+            const float b = __shfl_xor_sync(0xffffffffu, a, o);
+            a = MAX ? fmaxf(a, b) : a + b;
+        }
+    };
+    all();
     if (WARP) return;
     const int lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    if (lane == 0) sm[threadIdx.x >> 5] = make_float2(a, b);
+    if (lane == 0) sm[threadIdx.x >> 5] = a;
     __syncthreads();
-    const float2 v = lane < nw ? sm[lane] : make_float2(0.f, 0.f);
-    a = v.x;
-    b = v.y;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        if (MAX) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, o));
-    }
+    a = lane < nw ? sm[lane] : 0.f;                            // 0: a maximum is one of magnitudes
+    all();
 }
 
 __device__ __forceinline__ uint32_t codes2(float a, float b) {
@@ -105,7 +102,7 @@ __global__ void __launch_bounds__(VPT <= 2 || VEC == 1 ? 1024 : 512)
                    uint8_t* __restrict__ codes,
                    void* __restrict__ scales, float* __restrict__ rstd_out) {
     using P = Pack<T, VEC>;
-    __shared__ float2 sm[32];
+    __shared__ float sm[FMT == NORM_E4M3 ? 64 : 32];
     const int nv = d / VEC;
     const int width = WARP ? 32 : blockDim.x;
     const int me = WARP ? (threadIdx.x & 31) : threadIdx.x;
@@ -146,21 +143,27 @@ __global__ void __launch_bounds__(VPT <= 2 || VEC == 1 ? 1024 : 512)
         if (i < nv) wv[j] = wr[i];
         else wv[j].zero();
     }
-    float sq = 0.f, mx = 0.f;
+    float sq = 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const float f = s[j].get(e);
             sq = fmaf(f, f, sq);
-            if (FMT == NORM_E4M3) mx = fmaxf(mx, fabsf(f * wv[j].get(e)));
         }
-    reduce_row<WARP, FMT == NORM_E4M3>(sq, mx, sm);
+    reduce_row<WARP, false>(sq, sm);
     const float rstd = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sq, (float)d), eps)));
     if (rstd_out && me == 0) rstd_out[row] = rstd;
     float sc = 1.f;
     if (FMT == NORM_E4M3) {
-        sc = mx > 0.f ? fmaxf(__fdiv_rn(mx * rstd, 448.f), 1.17549435e-38f) : 1.f;      // at least 2^-126
+        // of the values themselves: s * w can leave fp32's range where s * rstd * w does not
+        float mx = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) mx = fmaxf(mx, fabsf(s[j].get(e) * rstd * wv[j].get(e)));
+        reduce_row<WARP, true>(mx, sm + 32);
+        sc = mx > 0.f ? fmaxf(__fdiv_rn(mx, 448.f), 1.17549435e-38f) : 1.f;      // at least 2^-126
         if (me == 0) static_cast<float*>(scales)[row] = sc;
     }
     const Divisor by(sc);
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(WARP ? 256 : VEC == 1 || VPT <= 2 ? 1024 : 512
                        float* __restrict__ partial) {
     using P = Pack<T, VEC>;
     extern __shared__ float smw[];                             // WARP: [warps][d] partial sums
-    __shared__ float2 sm[2][32];
+    __shared__ float sm[2][32];
     const int nv = d / VEC;
     const int width = WARP ? 32 : blockDim.x;
     const int me = WARP ? (threadIdx.x & 31) : threadIdx.x;
@@ -275,7 +278,7 @@ __global__ void __launch_bounds__(WARP ? 256 : VEC == 1 || VPT <= 2 ? 1024 : 512
             }
             r = rstd[row];
         }
-        float dot = 0.f, none = 0.f;
+        float dot = 0.f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(WARP ? 256 : VEC == 1 || VPT <= 2 ? 1024 : 512
                 dot = fmaf(g * wv[j].get(e), xh, dot);
                 acc[j][e] = fmaf(g, xh, acc[j][e]);
             }
-        reduce_row<WARP, false>(dot, none, sm[turn]);
+        reduce_row<WARP, false>(dot, sm[turn]);
         const float m = __fdiv_rn(dot, (float)d);
         P* dr = reinterpret_cast<P*>(dx + (size_t)row * d);
 #pragma unroll

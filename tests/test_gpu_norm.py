@@ -240,3 +240,15 @@ def test_codes_are_those_of_the_ieee_quotient(size):
     v = x.float() * o["rstd"][:, None] * w.float()
     assert torch.equal(o["y"], v.bfloat16())
     assert torch.equal((v / o["scale"][:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8), o["codes"])
+
+
+@pytest.mark.parametrize("rows", [2, 700])
+@pytest.mark.parametrize("d", [64, 2048])
+@pytest.mark.parametrize("s,w,eps", [(2.0 ** -100, 2.0 ** -60, 2.0 ** -100), (2.0 ** -80, 2.0 ** -75, 2.0 ** -80), (2.0 ** 55, 2.0 ** 75, 0.0),
+                                     (2.0 ** -100, 1.0, 1e-6), (0.0, 1.0, 1e-6), (1.0, 0.0, 1e-6)])
+def test_e4m3_scale_of_rows_whose_products_leave_fp32(rows, d, s, w, eps):
+    # s * w lies outside fp32's range, s * rstd * w does not (and rows of zeros or tiny numbers, which look alike)
+    x = (torch.randn(rows, d, generator=torch.Generator(device="cuda").manual_seed(4), device="cuda") * s).bfloat16()
+    x[0] = torch.randn(d, device="cuda").bfloat16() if w >= 0.5 else x[0]       # an ordinary row among them
+    _check_rows(moe.rmsnorm(x, torch.full((d,), w, device="cuda").bfloat16(), eps=eps, fmt=moe.FMT_E4M3), x, None,
+                torch.full((d,), w, device="cuda").bfloat16(), eps, moe.FMT_E4M3)
