@@ -568,7 +568,8 @@ def balance_stats(shape: MoeShape, x, centroids, counts, n_groups: int = 1, rout
     if n == 0:
         raise ValueError("layer shape not supported for balance statistics")
     if ws is None or ws.numel() < n:
-        ws = torch.zeros(n, dtype=torch.uint8, device=x.device)
+        with _scratch_of(stream):
+            ws = torch.zeros(n, dtype=torch.uint8, device=x.device)
     E = centroids.shape[0]
     f = torch.empty(E, dtype=torch.float32, device=x.device)
     P = torch.empty(E, dtype=torch.float32, device=x.device)
@@ -656,6 +657,12 @@ def _stream_of(dev: torch.device, stream=None):
 _SAME_DEVICE = contextlib.nullcontext()
 
 
+def _scratch_of(stream):
+    """Scratch that a call allocates and drops has to come from its own stream's memory: the current stream may be handed it
+    again as soon as the call returns, while the kernels still use it on the other stream."""
+    return _SAME_DEVICE if stream is None else torch.cuda.stream(stream)
+
+
 def _device_of(dev: torch.device):
     """Makes the tensors' device the current one for a call, where it is another."""
     return _SAME_DEVICE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
@@ -737,7 +744,9 @@ def rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, weight: torch.Tensor, rs
     _on_cuda(dev)
     dtype = MOE_BF16 if dt == torch.bfloat16 else MOE_F32
     n = int(_lib().moe_rmsnorm_backward_workspace_bytes(dtype, rows, d))
-    ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev) if ws is None else ws
+    if ws is None:
+        with _scratch_of(stream):
+            ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
     dx = torch.empty_like(s) if dx is None else dx
     dweight = torch.empty(d, dtype=torch.float32, device=dev) if dweight is None else dweight
     with _device_of(dev):
