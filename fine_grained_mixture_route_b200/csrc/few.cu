@@ -1464,7 +1464,9 @@ cudaError_t launch(Params& p, int grid, cudaStream_t st) {
     if (p.nst < 2) return cudaErrorInvalidValue;                // a consumer holds one stage while it waits for the next
     const Smem L(p.nst * p.stage, R * NT, p.T, p.E, p.k);
     auto kern = few_kernel<FR, NT, R>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L.total);
+    // The limit is the function's, for all host threads: always the same one, so that no thread lowers it between another's
+    // setting and launch.
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT);
     if (e != cudaSuccess) return e;
     void* args[] = {&p};
     return cudaLaunchCooperativeKernel(reinterpret_cast<const void*>(kern), dim3(grid), dim3(THREADS), args, L.total, st);

@@ -1,8 +1,12 @@
-"""Scratch buffers and streams: memory that a call allocates for itself while its kernels run on another stream."""
+"""Calls on several streams and from several host threads (B200): scratch that a call allocates for itself belongs to the
+stream it runs on, and threads with workspaces of their own do not disturb one another."""
+import threading
+
 import pytest
 import torch
 
 from fine_grained_mixture_route_b200 import moe
+from fine_grained_mixture_route_b200 import workloads as W
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +76,34 @@ def test_norm_backward_on_a_side_stream():
         torch.cuda.current_stream().wait_stream(side)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         side.wait_stream(torch.cuda.current_stream())
+
+
+def test_few_token_layers_from_two_host_threads():
+    # the same kernel with shared memory of two sizes (T and E differ), each thread with a stream and a workspace of its own
+    work, failed = [], []
+    for T, E, k in ((1, 4, 1), (8, 1024, 32)):
+        cfg = W.LayerConfig("few", T, 64, E, 32, k, 0, 0, True, torch.bfloat16, "normal_inv_sqrt_d")
+        L = W.make_layer(cfg, "cuda", T)
+        shape = moe.shape_of(L["x"], L["centroids"], L["routed"], k, None)
+        ws = moe.new_few_workspace(shape)
+        want = moe.layer_forward_few(shape, L["x"], L["centroids"], L["routed"], None, ws)
+        work.append((shape, L, ws, want, torch.empty_like(want), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    go = threading.Barrier(2)
+
+    def run(shape, L, ws, want, out, stream):
+        try:
+            go.wait(30)
+            for _ in range(300):
+                moe.layer_forward_few(shape, L["x"], L["centroids"], L["routed"], None, ws, out=out, stream=stream)
+            stream.synchronize()
+            assert torch.equal(out, want) and moe.check_device_error(ws, stream) == 0
+        except BaseException as e:                              # the main thread raises it
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not failed, failed
