@@ -168,8 +168,9 @@ __global__ void __launch_bounds__(THREADS) grad_norm_kernel(const __grid_constan
         *norm = nrm;
         st->done = 0u;
         if (max_norm >= 0.f) {
-            const float c = __fdiv_rn(max_norm, nrm + 1e-6f);
-            st->coef = c > 1.f ? 1.f : c;                       // a NaN norm stays NaN
+            // an infinite max_norm clips no norm, not even an infinite one; a NaN norm stays NaN
+            const float c = max_norm < INFINITY ? __fdiv_rn(max_norm, nrm + 1e-6f) : nrm >= 0.f ? 1.f : nrm;
+            st->coef = c > 1.f ? 1.f : c;
         }
     }
 }

@@ -830,7 +830,8 @@ def grad_norm(tensors, ws: torch.Tensor, norm: Optional[torch.Tensor] = None, st
 def clip_grads(tensors, max_norm: float, ws: torch.Tensor, out=None, norm: Optional[torch.Tensor] = None,
                stream=None) -> torch.Tensor:
     """moe_clip_grads: scales the tensors by min(1, max_norm / (norm + 1e-6)), in place or into the tensors of `out` (same
-    sizes and types), and returns the norm before clipping, an fp32 scalar on the device (no synchronisation)."""
+    sizes and types), and returns the norm before clipping, an fp32 scalar on the device (no synchronisation).  An infinite
+    max_norm clips nothing."""
     tensors = list(tensors)
     norm = _norm_out(norm, ws)
     arr, spans = _tensor_list(tensors, "tensors", ws.device)

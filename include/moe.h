@@ -543,7 +543,8 @@ typedef struct {
  * in place (and writes nothing when coef is 1), else tensors of the same sizes and types that do not
  * overlap the gradients of other entries.  Squares below fp32's range or above it are taken in 64 bits.
  * A norm of infinity gives coef 0 (infinite elements become NaN), a NaN norm gives NaN gradients.
- * max_norm must not be negative or NaN (infinity: no clipping).  No tensor may be listed twice.
+ * max_norm must not be negative or NaN.  With max_norm infinite nothing is clipped: coef is 1 for every norm, an
+ * infinite one included, but NaN for a NaN norm.  No tensor may be listed twice.
  * ws: moe_grad_workspace_bytes() bytes, cleared once by moe_ws_init; calls that share one must not overlap.
  * Sums in fixed order.
  */

@@ -132,3 +132,19 @@ def test_offsets_past_31_bits():
     ws = moe.new_grad_workspace()
     assert float(moe.clip_grads([t], 1.0, ws)) == 13.0
     _check_scaled([t[-3:]], [torch.tensor([3.0, 4.0, 12.0], device="cuda").bfloat16()], _coef(13.0, 1.0))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_no_clipping_of_an_infinite_norm(dtype):
+    ws = moe.new_grad_workspace()
+    one = torch.ones(1000, device="cuda", dtype=dtype)          # an infinite gradient
+    one[3] = float("inf")
+    large = torch.full((1000,), 3e38, device="cuda", dtype=dtype)       # finite ones whose norm is beyond fp32
+    for t in (one, large):
+        mine, out = t.clone(), torch.zeros_like(t)
+        assert float(moe.clip_grads([mine], math.inf, ws)) == math.inf and torch.equal(mine, t)
+        assert float(moe.clip_grads([t], math.inf, ws, out=[out])) == math.inf and torch.equal(out, t)
+    one[5] = float("nan")
+    assert math.isnan(float(moe.clip_grads([one], math.inf, ws))) and torch.isnan(one).all()
+    small = torch.zeros(10, device="cuda", dtype=dtype)
+    assert float(moe.clip_grads([small], math.inf, ws)) == 0.0 and (small == 0).all()
