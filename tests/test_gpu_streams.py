@@ -1,5 +1,6 @@
 """Calls on several streams and from several host threads (B200): scratch that a call allocates for itself belongs to the
 stream it runs on, and threads with workspaces of their own do not disturb one another."""
+import ctypes
 import threading
 
 import pytest
@@ -79,31 +80,32 @@ def test_norm_backward_on_a_side_stream():
 
 
 def test_few_token_layers_from_two_host_threads():
-    # the same kernel with shared memory of two sizes (T and E differ), each thread with a stream and a workspace of its own
-    work, failed = [], []
+    # the same kernel with shared memory of two sizes (T and E differ), each thread with a stream and a workspace of its own.
+    # The C entry point, without the interpreter's work between calls, so that the threads' calls overlap
+    lib, work = moe.lib_handle(), []
     for T, E, k in ((1, 4, 1), (8, 1024, 32)):
         cfg = W.LayerConfig("few", T, 64, E, 32, k, 0, 0, True, torch.bfloat16, "normal_inv_sqrt_d")
         L = W.make_layer(cfg, "cuda", T)
         shape = moe.shape_of(L["x"], L["centroids"], L["routed"], k, None)
         ws = moe.new_few_workspace(shape)
         want = moe.layer_forward_few(shape, L["x"], L["centroids"], L["routed"], None, ws)
-        work.append((shape, L, ws, want, torch.empty_like(want), torch.cuda.Stream()))
+        out, stream, w = torch.empty_like(want), torch.cuda.Stream(), moe._weights(L["routed"])
+        args = (ctypes.byref(shape), L["x"].data_ptr(), L["centroids"].data_ptr(), None, ctypes.byref(w), None, out.data_ptr(),
+                None, None, None, ws.data_ptr(), ws.numel(), stream.cuda_stream)
+        work.append(dict(args=args, keep=(shape, L, w), ws=ws, want=want, out=out, stream=stream, status=[]))
     torch.cuda.synchronize()
     go = threading.Barrier(2)
 
-    def run(shape, L, ws, want, out, stream):
-        try:
-            go.wait(30)
-            for _ in range(300):
-                moe.layer_forward_few(shape, L["x"], L["centroids"], L["routed"], None, ws, out=out, stream=stream)
-            stream.synchronize()
-            assert torch.equal(out, want) and moe.check_device_error(ws, stream) == 0
-        except BaseException as e:                              # the main thread raises it
-            failed.append(e)
+    def run(w):
+        go.wait(30)
+        w["status"] += [lib.moe_layer_forward_few(*w["args"]) for _ in range(5000)]
 
-    threads = [threading.Thread(target=run, args=w) for w in work]
+    threads = [threading.Thread(target=run, args=(w,)) for w in work]
     for t in threads:
         t.start()
     for t in threads:
         t.join(60)
-    assert not failed, failed
+    torch.cuda.synchronize()
+    for w in work:
+        assert len(w["status"]) == 5000 and set(w["status"]) == {moe.MOE_OK}
+        assert torch.equal(w["out"], w["want"]) and moe.check_device_error(w["ws"]) == 0
