@@ -31,8 +31,9 @@
 // 8-bit codes become fp16, exactly and in one instruction a pair (bf16 takes four, and the conversions then
 // bound the kernel: 185 us instead of 165 for w1, w3 of 22 block-scaled experts of 2048 x 7168).  Their
 // activations are therefore fp16 too, each row times a power of two that brings its largest finite value into
-// [2^14, 2^15): x in one number (its 8 bits are kept down to 2^-28 of that, and 2^-40 of it is the largest error), h in
-// two (22 bits of its fp32 value), for which the rows' largest values have to be known: one grid barrier more, behind
+// [2^14, 2^15), below 2^-112 times 2^126: x in one number, h in two (22 bits of its fp32 value).  fp16's smallest step is
+// 2^-24, so a row is off by at most 2^-25 / 2^14 = 2^-39 of its largest value (below 2^-112: by 2^-151), and x keeps its
+// 8 bits down to 2^-31 of it.  For h the rows' largest values have to be known: one grid barrier more, behind
 // which the rows are converted, while the first weights of w2 arrive.
 // A thread's k-columns need only be the same for both operands, so every fragment is a plain 16- or 8-byte
 // load, without ldmatrix.

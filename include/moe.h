@@ -562,7 +562,8 @@ moe_status_t moe_clip_grads(const moe_tensor_t* grads, const moe_tensor_t* out, 
  * everywhere, but the activations are NOT quantised: with few tokens nothing is gained by it, and the
  * result is the layer's on the dequantised weights.  So it can differ from moe_layer_forward's, which
  * quantises them, by that quantisation.  Hidden values are fp32; for FP8 experts they are read with 22
- * significant bits, and a row of x or of hidden values is accurate to 2^-40 of its largest value at least.
+ * significant bits, and a row of x or of hidden values is accurate to 2^-39 of its largest finite value, or
+ * to 2^-151 where that is below 2^-112.
  * Sums are fp32, in an order that depends on sizes and picks alone.
  * A pick that does not exist (NaN logits, or all other keys -infinity) sets error bit 1 and is left out.
  * Sizes: as the layer's, T <= MOE_FEW_MAX_TOKENS, d <= 32768, and for MOE_F32 d, inter and inter_shared

@@ -1,4 +1,6 @@
 """The whole layer for a few tokens (moe.layer_forward_few) against the 64-bit definition (B200)."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -338,3 +340,28 @@ def test_infinite_hidden_values_stay_infinite(fmt):
     keep = torch.arange(64, device="cuda") != 9
     assert torch.equal(out[0, keep], sign[keep] * float("inf")) and torch.isnan(out[0, 9])
     assert torch.isfinite(out[1]).all() and (out[1, keep] != 0).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "mxfp8"])
+@pytest.mark.parametrize("largest,rel", [(m, r) for m in (1.0, 1.9921875, 2.0 ** -90) for r in (1.0, 1.25, 1.5, 1.9921875, 33.0, 2.0 ** 20)] +
+                         [(2.0 ** -100, r) for r in (65.0, 2.0 ** 12, 2.0 ** 20)] +       # not below bf16's subnormal step, 2^-133
+                         [(m, r) for m in (2.0 ** -112, 2.0 ** -118) for r in (2.0 ** 18, 7.0 * 2.0 ** 18, 2.0 ** 25)])
+def test_small_values_beside_a_large_one(fmt, largest, rel):
+    # x = (largest, v) with v at rel times the bound below which a value may be lost: h = silu(w v) * b3 with w near 2^-30 / v
+    bound = 2.0 ** -39 * largest if largest >= 2.0 ** -112 else 2.0 ** -151
+    v = float(torch.tensor(rel * bound, dtype=torch.float64).bfloat16())
+    assert v > 0.0
+    w = 2.0 ** (-30 - math.frexp(v)[1])
+    L = _case(T=1, d=64, E=1, I=16, k=1)
+    s = L["routed"]
+    for n in ("w1", "w3", "w2", "b1", "b3", "b2"):
+        s[n].zero_()
+    L["x"].zero_()
+    L["x"][0, 0], L["x"][0, 40] = largest, v
+    s["w1"][0, 3, 40], s["b3"][0, 3], s["w2"][0, :, 3] = w, 1.0, 1.0
+    assert torch.isfinite(s["w1"]).all()
+    L["routed"] = quant.quantize_stack(s, fmt)
+    o = _run(L)
+    ref, _ = R.few_layer(L["x"], o["idx"], o["gate"], L["routed"], None, 0)
+    # |silu'| is about 1/2 there; a bf16 result, and 2^-20 for the 22 bits of h and the scales' products
+    assert ((o["out"].double() - ref).abs() <= 0.51 * w * bound + (2.0 ** -8 + 2.0 ** -20) * ref.abs()).all()
