@@ -273,7 +273,7 @@ constexpr int NORM_MAX_D = 16384;
 cudaError_t launch_rmsnorm(bool bf16, int fmt, const void* x, const void* res, const void* w, float eps, long long rows,
                            int d, void* sum, void* y, uint8_t* codes, void* scales, float* rstd, cudaStream_t stream);
 // dx and dweight [d]; partial: norm_bwd_partials(rows) rows of d fp32.  dsum may be NULL.
-constexpr int NORM_BWD_BLOCKS = 296;
+constexpr int NORM_BWD_BLOCKS = 296;          // 2 on each of 148 SMs
 int norm_bwd_partials(long long rows);
 cudaError_t launch_rmsnorm_bwd(bool bf16, const void* dy, const void* s, const void* w, const float* rstd, const void* dsum,
                                long long rows, int d, void* dx, float* dweight, float* partial, cudaStream_t stream);

@@ -419,7 +419,10 @@ cudaError_t bwd_shape(const BwdArgs& a, int* blocks, cudaStream_t st) {
         return nv <= 32 ? bwd_launch<T, VEC, 1, true>(a, 256, *blocks, st)
                         : bwd_launch<T, VEC, 4, true>(a, 256, *blocks, st);
     }
-    if (VEC > 1 && nv <= 1024) {                               // as many blocks as fit, with 64 registers a thread
+    // As many blocks as fit with 64 registers a thread, but at most NORM_BWD_BLOCKS, which binds below 512 threads.  Twice as
+    // many partial rows would suit many narrow rows (16384 of 1280: 47 us instead of 59, of 2048: 57 instead of 70) and
+    // cost few rows, and the widest (700 of 2048: 18 instead of 14; 700 of 16384: 80 instead of 55).
+    if (VEC > 1 && nv <= 1024) {
         const int threads = round32(nv), fit = num_sms() * (1024 / threads);
         if (*blocks > fit) *blocks = fit;
         return bwd_launch<T, VEC, 1, false>(a, threads, *blocks, st);

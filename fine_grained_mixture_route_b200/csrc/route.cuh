@@ -1,5 +1,5 @@
-// Ranking of one token's router logits by one warp, shared by the CUDA-core router, the split-K
-// router's last step and the few-token layer.
+// Ranking of one token's router logits by one warp, for the CUDA-core router and the split-K router's last step.  (The
+// few-token layer ranks by the same rules in a form of its own, made for latency.)
 #pragma once
 
 #include "common.cuh"

@@ -694,7 +694,7 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: 
     """moe_rmsnorm: RMS norm of x [rows, d], or of x + residual.  Returns {"y", "sum" (the rounded x + residual, the
     residual stream from here on; None without one), "rstd" (fp32 [rows], for the backward pass), "codes", "scale"}: with
     fmt FMT_E4M3 uint8 codes [rows, d] and fp32 scales [rows], with FMT_MXFP8 codes and scale bytes
-    [rows, ceil(d / 32)] (layer_forward's x_quant), else None.  `out` may hold these tensors; out["sum"] may be
+    [rows, ceil(d / 32)] (layer_forward_quantized's x_codes and x_scale), else None.  `out` may hold these tensors; out["sum"] may be
     residual itself."""
     _rows(x, "x")
     rows, d = x.shape
