@@ -365,8 +365,7 @@ MOE_EXPORT moe_status_t moe_check_device_error(void* ws, size_t ws_bytes, moe_st
     if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
     if (detail) *detail = h;
     if (h) {
-        // the whole header: a few-token kernel that gave up leaves its grid barriers between two rounds
-        if (cudaMemsetAsync(ws, 0, 256, st) != cudaSuccess) return MOE_ERR_CUDA;
+        if (cudaMemsetAsync(ws, 0, sizeof(h), st) != cudaSuccess) return MOE_ERR_CUDA;
         if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
         return MOE_ERR_INTERNAL;
     }

@@ -573,8 +573,8 @@ moe_status_t moe_clip_grads(const moe_tensor_t* grads, const moe_tensor_t* out, 
  * moe_ws_init: the kernel's grid barriers count in it from call to call.  A workspace serves any supported
  * shape that needs at most its size.  Calls that share one must not overlap.  The kernel is launched
  * cooperatively, a block on every SM: it starts when the stream's turn comes and all SMs are free.
- * Every wait is bounded; one that gives up sets error bit 2, and moe_check_device_error then clears the
- * barriers too.  Can be captured into a graph.
+ * Every wait is bounded, and one that gives up sets error bit 2.  Every block arrives at every barrier on all
+ * paths, so that the workspace is as good as before after an error.  Can be captured into a graph.
  */
 #define MOE_FEW_MAX_TOKENS 16
 size_t moe_few_workspace_bytes(const moe_shape_t* shape);

@@ -365,3 +365,22 @@ def test_small_values_beside_a_large_one(fmt, largest, rel):
     ref, _ = R.few_layer(L["x"], o["idx"], o["gate"], L["routed"], None, 0)
     # |silu'| is about 1/2 there; a bf16 result, and 2^-20 for the 22 bits of h and the scales' products
     assert ((o["out"].double() - ref).abs() <= 0.51 * w * bound + (2.0 ** -8 + 2.0 ** -20) * ref.abs()).all()
+
+
+@pytest.mark.parametrize("fmt", [None, "mxfp8"])
+def test_a_workspace_after_an_error(fmt):
+    # barriers are counts of arrivals that only grow: whole rounds of them after a call that flagged an error, also once the
+    # error word has been read, which clears that word alone
+    L = _case(T=3, d=64, E=6, I=32, k=2, Ks=1, fmt=fmt)
+    ws = _run(L)["ws"]
+    want = _run(L, ws=ws)["out"]
+    x = L["x"].clone()
+    x[1] = float("nan")
+    blocks = torch.cuda.get_device_properties(0).multi_processor_count
+    for calls in (3, 5):
+        _run(L, ws=ws, x=x)
+        with pytest.raises(moe.MoeError):
+            moe.check_device_error(ws)
+        assert ws[64:88].view(torch.int64).tolist() == [calls * blocks, calls * blocks, calls * blocks if fmt else 0]
+        o = _run(L, ws=ws)
+        assert torch.equal(o["out"], want) and moe.check_device_error(ws) == 0
