@@ -772,12 +772,12 @@ def new_grad_workspace(device="cuda") -> torch.Tensor:
     return ws
 
 
-_GRAD_TYPES = {torch.bfloat16: (MOE_BF16, 2), torch.float32: (MOE_F32, 4)}   # moe_dtype_t, bytes
+_GRAD_TYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
 
 
 def _tensor_list(tensors, name: str, device: torch.device):
-    """(descriptors for the C entry points, [(first byte, end, index)] of the tensors that hold elements)."""
-    flat, spans = [], []                                        # moe_tensor_t: pointer, int64, int32 and padding
+    """Descriptors for the C entry points."""
+    flat, index = [], -1 if device.index is None else device.index      # moe_tensor_t: pointer, int64, int32 and padding
     for i, t in enumerate(tensors):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}[{i}] must be a torch.Tensor")
@@ -786,18 +786,16 @@ def _tensor_list(tensors, name: str, device: torch.device):
             raise ValueError(f"{name}[{i}] has dtype {t.dtype}; bfloat16 or float32 is needed")
         if not t.is_contiguous():
             raise ValueError(f"{name}[{i}] must be contiguous")
-        if t.device != device:
+        if t.get_device() != index:                             # -1: not on a GPU
             raise ValueError(f"{name}[{i}] is on {t.device}; the workspace is on {device}")
-        p, n = t.data_ptr(), t.numel()
-        flat += (p, n, kind[0])
-        if n:
-            spans.append((p, p + n * kind[1], i))
+        flat += (t.data_ptr(), t.numel(), kind)
     flat = array.array("q", flat or (0, 0, 0))
-    return (MoeTensor * (len(flat) // 3)).from_buffer(flat), spans
+    return (MoeTensor * (len(flat) // 3)).from_buffer(flat)
 
 
 def _spans(tensors):
-    return [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i) for i, t in enumerate(tensors) if t.numel()]
+    """[(first byte, end, index)] of the tensors that hold elements."""
+    return [(p := t.data_ptr(), p + n, i) for i, t in enumerate(tensors) if (n := t.nbytes)]
 
 
 def _no_overlap(spans, what: str):
@@ -807,10 +805,13 @@ def _no_overlap(spans, what: str):
             raise ValueError(f"{what} {a[2]} and {b[2]} overlap in memory")
 
 
-def _norm_out(norm, ws):
+def _need_norm(norm, ws):
     if not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8:
         raise TypeError("ws must be a workspace of new_grad_workspace")
     _need(norm, "norm", 1, torch.float32, ws.device)
+
+
+def _norm_out(norm, ws):
     _on_cuda(ws.device)
     return torch.empty((), dtype=torch.float32, device=ws.device) if norm is None else norm
 
@@ -819,8 +820,9 @@ def grad_norm(tensors, ws: torch.Tensor, norm: Optional[torch.Tensor] = None, st
     """moe_grad_norm: the L2 norm over all elements of a list of bf16 and fp32 tensors, an fp32 scalar on the device (no
     synchronisation).  ws from new_grad_workspace."""
     tensors = list(tensors)
+    _need_norm(norm, ws)
+    arr = _tensor_list(tensors, "tensors", ws.device)
     norm = _norm_out(norm, ws)
-    arr, _ = _tensor_list(tensors, "tensors", ws.device)
     with _device_of(ws.device):
         _check(_lib().moe_grad_norm(arr, len(tensors), _ptr(norm), _ptr(ws), ws.numel(), _stream_of(ws.device, stream)),
                "moe_grad_norm")
@@ -833,18 +835,19 @@ def clip_grads(tensors, max_norm: float, ws: torch.Tensor, out=None, norm: Optio
     sizes and types), and returns the norm before clipping, an fp32 scalar on the device (no synchronisation).  An infinite
     max_norm clips nothing."""
     tensors = list(tensors)
-    norm = _norm_out(norm, ws)
-    arr, spans = _tensor_list(tensors, "tensors", ws.device)
+    _need_norm(norm, ws)
+    arr, spans = _tensor_list(tensors, "tensors", ws.device), _spans(tensors)
     oarr = None
     if out is None:
         _no_overlap(spans, "tensors")
     else:
         out = list(out)
-        oarr, ospans = _tensor_list(out, "out", ws.device)
+        oarr = _tensor_list(out, "out", ws.device)
         if len(out) != len(tensors) or any(o.shape != t.shape or o.dtype != t.dtype for o, t in zip(out, tensors)):
             raise ValueError("out must hold a tensor of the same shape and type for each gradient")
         # an output may be its gradient itself, and overlaps nothing else
-        _no_overlap(spans + [o for o, t in zip(ospans, spans) if o[:2] != t[:2]], "gradients or out")
+        _no_overlap(spans + [o for o, t in zip(_spans(out), spans) if o[:2] != t[:2]], "gradients or out")
+    norm = _norm_out(norm, ws)
     with _device_of(ws.device):
         _check(_lib().moe_clip_grads(arr, oarr, len(tensors), float(max_norm), _ptr(norm), _ptr(ws), ws.numel(),
                                      _stream_of(ws.device, stream)), "moe_clip_grads")

@@ -63,6 +63,33 @@ def test_grad_lists_refused():
     moe._no_overlap(moe._spans([t[:50], t[50:], t[:0]]), "tensors")
 
 
+def test_clipping_refuses_what_overlaps():
+    ws, t = torch.zeros(1 << 14, dtype=torch.uint8), torch.zeros(100)
+    a, b, e = t[:40], t[40:80], t[:0]
+
+    def clip(ts, out=None):
+        return moe.clip_grads(ts, 1.0, ws, out=out)
+
+    for ts in ([t, t], [t[:50], t[49:]], [a, b, t[79:81]], [b, a, t], [t[10:20], e, t[:11]], [t.view(torch.int32).view(torch.float32), t]):
+        with pytest.raises(ValueError, match="overlap"):
+            clip(ts)
+    o = torch.zeros(100)
+    for out in ([b, a],                                         # another gradient's place
+                [a, t[39:79]],                                  # its own gradient, one element off, and the one before
+                [t[1:41], o[:40]],                              # its own gradient, one element off
+                [o[:40], o[39:79]], [o[:40], o[:40]], [a, a]):  # one another, or another output that is a gradient
+        with pytest.raises(ValueError, match="overlap"):
+            clip([a, b], out)
+    for out in ([o[:40]], [o[:40], o[40:81]], [o[:40], o[40:80].bfloat16()]):
+        with pytest.raises(ValueError, match="same shape and type"):
+            clip([a, b], out)
+    # allowed as far as the overlap goes: the gradients themselves, some of them, neighbours, empty ones anywhere
+    for ts, out in (([a, b], None), ([a, b], [a, b]), ([a, b], [a, o[:40]]), ([a, b], [o[:40], o[40:80]]), ([e, a, e, b], None),
+                    ([a, e, b], [a, t[20:20], t[80:].new_zeros(40)]), ([], None), ([], [])):
+        with pytest.raises(ValueError, match="CUDA"):
+            clip(ts, out)
+
+
 def test_c_entry_points_return_errors():
     lib, INV, UNS, WS = moe.lib_handle(), moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED, moe.MOE_ERR_WORKSPACE
     p, odd = ctypes.c_void_p(1 << 40), ctypes.c_void_p((1 << 40) + 8)      # never dereferenced
