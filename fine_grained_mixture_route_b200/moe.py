@@ -778,10 +778,11 @@ _GRAD_TYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
 def _tensor_list(tensors, name: str, device: torch.device):
     """Descriptors for the C entry points."""
     flat, index = [], -1 if device.index is None else device.index      # moe_tensor_t: pointer, int64, int32 and padding
+    tensor, kind_of = torch.Tensor, _GRAD_TYPES.get
     for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor):
+        if not isinstance(t, tensor):
             raise TypeError(f"{name}[{i}] must be a torch.Tensor")
-        kind = _GRAD_TYPES.get(t.dtype)
+        kind = kind_of(t.dtype)
         if kind is None:
             raise ValueError(f"{name}[{i}] has dtype {t.dtype}; bfloat16 or float32 is needed")
         if not t.is_contiguous():
@@ -799,10 +800,11 @@ def _spans(tensors):
 
 
 def _no_overlap(spans, what: str):
-    spans = sorted(spans)
-    for a, b in zip(spans, spans[1:]):
-        if b[0] < a[1]:
-            raise ValueError(f"{what} {a[2]} and {b[2]} overlap in memory")
+    end, before = 0, None                                       # of the tensor before
+    for first, last, i in sorted(spans):
+        if first < end:
+            raise ValueError(f"{what} {before} and {i} overlap in memory")
+        end, before = last, i
 
 
 def _need_norm(norm, ws):
@@ -846,7 +848,7 @@ def clip_grads(tensors, max_norm: float, ws: torch.Tensor, out=None, norm: Optio
         if len(out) != len(tensors) or any(o.shape != t.shape or o.dtype != t.dtype for o, t in zip(out, tensors)):
             raise ValueError("out must hold a tensor of the same shape and type for each gradient")
         # an output may be its gradient itself, and overlaps nothing else
-        _no_overlap(spans + [o for o, t in zip(_spans(out), spans) if o[:2] != t[:2]], "gradients or out")
+        _no_overlap(spans + [o for o, t in zip(_spans(out), spans) if o != t], "gradients or out")
     norm = _norm_out(norm, ws)
     with _device_of(ws.device):
         _check(_lib().moe_clip_grads(arr, oarr, len(tensors), float(max_norm), _ptr(norm), _ptr(ws), ws.numel(),
