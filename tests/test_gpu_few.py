@@ -384,3 +384,28 @@ def test_a_workspace_after_an_error(fmt):
         assert ws[64:88].view(torch.int64).tolist() == [calls * blocks, calls * blocks, calls * blocks if fmt else 0]
         o = _run(L, ws=ws)
         assert torch.equal(o["out"], want) and moe.check_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("fmt", [None, "e4m3", "mxfp8"])
+@pytest.mark.parametrize("T", [2, 5, 11])
+def test_experts_read_an_infinite_row(fmt, T):
+    # sigmoid gates: every key of the infinite row is 1 + bias, so that experts are picked and read it.  All of its hidden
+    # values are infinite, and w2's rows have one sign each: infinite results of that sign.  The other tokens keep their bits
+    L = _case(T=T, d=272, E=8, I=48, k=3, Ks=1, bias=False, mode=2)
+    L["centroids"][:, 7] = 2.0 ** -6
+    sign = torch.where(torch.arange(272, device="cuda") % 3 == 0, -1.0, 1.0)
+    for n in ("routed", "shared"):
+        s = L[n]
+        s["w1"][:, :, 7], s["w3"][:, :, 7] = 1.0, 1.0
+        s["w2"].copy_((0.5 + s["w2"].float().abs().clamp(max=1.0)) * sign[None, :, None])
+    if fmt:
+        L["routed"] = quant.quantize_stack(L["routed"], fmt)
+    want = _run(L)
+    x = L["x"].clone()
+    x[T - 1, 7] = float("inf")
+    o = _run(L, x=x)
+    assert moe.check_device_error(o["ws"]) == 0
+    assert torch.equal(o["out"][:-1], want["out"][:-1]) and torch.equal(o["idx"][:-1], want["idx"][:-1])
+    top = torch.sort(L["router_bias"], descending=True, stable=True).indices[:3]
+    assert torch.equal(o["idx"][-1].long(), top) and ((o["gate"][-1] - 1 / 3).abs() <= 2.0 ** -22).all()
+    assert torch.equal(o["out"][-1].float(), sign * float("inf"))

@@ -252,3 +252,31 @@ def test_e4m3_scale_of_rows_whose_products_leave_fp32(rows, d, s, w, eps):
     x[0] = torch.randn(d, device="cuda").bfloat16() if w >= 0.5 else x[0]       # an ordinary row among them
     _check_rows(moe.rmsnorm(x, torch.full((d,), w, device="cuda").bfloat16(), eps=eps, fmt=moe.FMT_E4M3), x, None,
                 torch.full((d,), w, device="cuda").bfloat16(), eps, moe.FMT_E4M3)
+
+
+@pytest.mark.parametrize("fmt", [moe.FMT_NATIVE, moe.FMT_E4M3, moe.FMT_MXFP8])
+@pytest.mark.parametrize("d", [264, 1536, 7168])
+def test_a_row_alone_is_the_row_among_others(fmt, d):
+    # one row takes another split over the threads than 400 do: the sums' order differs, and with it rstd by 2 F32 at most.
+    # Both results are then within half a step of values that far apart: a whole step of y, and of the codes' values
+    x, res, w = _inputs(400, d, torch.bfloat16)
+    all_ = moe.rmsnorm(x, w, residual=res, fmt=fmt)
+    for i in (0, 17, 399):
+        one = moe.rmsnorm(x[i:i + 1].clone(), w, residual=res[i:i + 1].clone(), fmt=fmt)
+        assert torch.equal(one["sum"][0], all_["sum"][i])
+        r = all_["rstd"][i].double()
+        assert (one["rstd"][0].double() - r).abs() <= 2 * R.F32 * r
+        v = (all_["sum"][i].double() * r * w.double()).abs()
+        assert ((one["y"][0].double() - all_["y"][i].double()).abs() <= (2 * R.HALF[torch.bfloat16] + 4 * R.F32) * v).all()
+        if fmt == moe.FMT_NATIVE:
+            continue
+        q = [o.view(torch.float8_e4m3fn).double() for o in (one["codes"][0], all_["codes"][i])]
+        if fmt == moe.FMT_E4M3:
+            s = [one["scale"][0].double(), all_["scale"][i].double()]
+            assert (s[0] - s[1]).abs() <= 4 * R.F32 * s[1]
+        else:
+            e = [one["scale"][0].double() - 127, all_["scale"][i].double() - 127]
+            assert ((e[0] - e[1]).abs() <= 1).all() and (e[0] != e[1]).sum() <= 1      # next to a border of the exponent only
+            s = [torch.pow(2.0, k).repeat_interleave(32)[:d] for k in e]
+        step = torch.maximum(*s) if fmt == moe.FMT_MXFP8 else s[1]
+        assert ((q[0] * s[0] - q[1] * s[1]).abs() <= (2 * 2.0 ** -4 + 8 * R.F32) * v + 2 * 2.0 ** -10 * step).all()
