@@ -231,33 +231,14 @@ __device__ __forceinline__ uint4 lds128(const char* a) { return *reinterpret_cas
 // With an infinite number or NaN among its columns a first part's sum is not finite, and stands alone.
 __device__ __forceinline__ float add_parts(float first, float others) { return fabsf(first) < INFINITY ? first + others : first; }
 
-// 8 fp32 numbers as the sum of three bf16 ones, exactly: each part is the upper half of what is left, its top 8 bits.
-// Of an infinite number or NaN the first part is one too, and the others mean nothing.
-__device__ __forceinline__ void bf16_parts(const uint4 (&v)[2], uint4 (&part)[3]) {
-    const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-    uint32_t o[3][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t a = w[2 * i], b = w[2 * i + 1];
-#pragma unroll
-        for (int q = 0; q < 3; ++q) {
-            o[q][i] = __byte_perm(a, b, 0x7632);
-            if (q == 2) break;
-            a = __float_as_uint(__uint_as_float(a) - __uint_as_float(a & 0xFFFF0000u));
-            b = __float_as_uint(__uint_as_float(b) - __uint_as_float(b & 0xFFFF0000u));
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < 3; ++q) part[q] = make_uint4(o[q][0], o[q][1], o[q][2], o[q][3]);
-}
-
 // A thread's fragments of a stage: 16 R weight rows and up to 8 NT tokens over the warp's columns, wk from the
 // stage's start and kb < K of all.  act[nt]: where the thread's token's row is in the stage (0: the token is not
-// among the unit's); HL = 1: a row of x, HL = 2: one of h.  Columns past K hold an earlier stage's bytes:
+// among the unit's); HL = 1: a row of x, HL = 2: one of h beside 8-bit weights.  Columns past K hold an earlier stage's bytes:
 // both operands are zeroed.  sf: the scale bytes of the warp's 2 runs.
 template <int FR, int F, int NT, int HL, int R>
 struct Frag {
     using L = Fmt<FR, F>;
+    static_assert(F != W_BF16 || HL == 1, "h beside 16-bit weights is unit_parts'");
     static constexpr int STEPS = L::PER_WARP / 32;
     using A = typename std::conditional<F == W_BF16, uint4, uint2>::type;
     A a[STEPS][R][2];
@@ -299,28 +280,19 @@ struct Frag {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 if (NT > 1 && ((mask >> (8 * nt)) & 0xFFu) == 0u) continue;
-                constexpr int PARTS = HL > 1 ? 3 : 1;
-                float t[PARTS][R][4] = {};                      // one for each part: short chains of products
+                float t[R][4] = {};
 #pragma unroll
-                for (int s = 0; s < STEPS; ++s) {
-                    uint4 v[PARTS];
-                    if constexpr (HL > 1) bf16_parts(b[s][nt], v);
-                    else v[0] = b[s][nt][0];
+                for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-                    for (int q = 0; q < PARTS; ++q)
-#pragma unroll
-                        for (int i = 0; i < R; ++i) {
-                            const uint4 &a0 = a[s][i][0], &a1 = a[s][i][1];
-                            mma_bf16(t[q][i], a0.x, a1.x, a0.y, a1.y, v[q].x, v[q].y);
-                            mma_bf16(t[q][i], a0.z, a1.z, a0.w, a1.w, v[q].z, v[q].w);
-                        }
-                }
+                    for (int i = 0; i < R; ++i) {
+                        const uint4 &a0 = a[s][i][0], &a1 = a[s][i][1], &v = b[s][nt][0];
+                        mma_bf16(t[i], a0.x, a1.x, a0.y, a1.y, v.x, v.y);
+                        mma_bf16(t[i], a0.z, a1.z, a0.w, a1.w, v.z, v.w);
+                    }
 #pragma unroll
                 for (int i = 0; i < R; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        acc[i][nt * 4 + j] += HL > 1 ? add_parts(t[0][i][j], t[PARTS > 1][i][j] + t[PARTS - 1][i][j]) : t[0][i][j];
-                    }
+                    for (int j = 0; j < 4; ++j) acc[i][nt * 4 + j] += t[i][j];
             }
         } else {
             float2 f[R][2];
@@ -425,78 +397,124 @@ __device__ __forceinline__ void unit_mma(float (&acc)[R][NT * 4], Me& me, int sf
     }
 }
 
-// A unit of the down-projection with 16-bit weights and one or two tokens, as most units of routed experts have: the parts
-// of h take the free columns of the products, which makes a third of them (16 tokens on 64 experts of 1408 x 2048: 191 us
-// instead of 202).  Column 4 j + q is part q of the unit's token j.  t: as unit_mma's.  Layers with 8-bit experts have only
-// their shared ones here, and the registers are worth more to the others (four tokens, e4m3: 264 us instead of 256).
-template <int FR, int NT, int R>
+// A unit of the down-projection with 16-bit weights and up to TOK tokens, t as unit_mma's.  Every fp32 number of h is the sum of
+// three bf16 ones, exactly: each part is the upper half of what the parts before leave, its top 8 bits.  (Of an infinite number or
+// NaN the first part is one too, and the others mean nothing.)  The unit's tokens stand in order in the products' columns, so
+// that 9 to 16 tokens of the layer take a second group of columns only in units that have as many.  With one or two tokens, as most
+// units of routed experts have, the parts take the free columns: column 4 j + q is part q of token j, a third of the products;
+// else column j is token j and each part has products of its own.  (16 tokens, alternating inputs: 64 experts of 1408 x 2048
+// 178 us, 202 with products for every part and columns by the layer's tokens; 32 experts of 2048 x 7168 484 us, 555 with the
+// columns by the layer's tokens.)
+template <int FR, int NT, int R, int TOK>
 __device__ __forceinline__ void unit_parts(float (&t)[R][NT * 4], Me& me, int K, uint32_t mask) {
     using L = Fmt<FR, W_BF16>;
-    constexpr int STEPS = L::PER_WARP / 32;
-    const int wk = me.warp * L::PER_WARP, g = me.lane >> 2, c = (me.lane & 3) * 8, j = g >> 2, q = g & 3;
-    const bool mine = j < __popc(mask) && q < 3;
+    constexpr int STEPS = L::PER_WARP / 32, COLS = TOK == 2 ? 4 : 1, SETS = TOK == 2 ? 1 : 3, GROUPS = TOK > 8 ? 2 : 1;
+    const int wk = me.warp * L::PER_WARP, g = me.lane >> 2, c = (me.lane & 3) * 8, q = g % COLS, n = __popc(mask);
     const char* row = me.sm + g * L::PITCH;
-    const int act = Stage<FR, R>::acts + j * hrow<FR, W_BF16>();
-    const uint32_t m1 = q > 0 ? 0xFFFF0000u : 0u, m2 = q > 1 ? 0xFFFF0000u : 0u;    // what the parts before hold
-    float acc[R][4] = {};
+    const uint32_t up = 0xFFFF0000u, m1 = q > 0 ? up : 0u, m2 = q > 1 ? up : 0u;     // what the parts before a column's hold
+    auto rest = [](uint32_t w, uint32_t m) { return __float_as_uint(__uint_as_float(w) - __uint_as_float(w & m)); };
+    float acc[GROUPS][R][4] = {};
     for (int k0 = 0; k0 < K; k0 += L::KS) {
         wait_full(me, me.ring);
         if (k0 + wk < K) {
+            const char* stage = me.sm + me.ring.slot * me.ring.stage + Stage<FR, R>::acts;
             const int at = me.ring.slot * me.ring.stage;
-            uint4 a[STEPS][R][2], v[STEPS][2];
+            uint4 a[STEPS][R][2], v[GROUPS][STEPS][2];
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int k = wk + s * 32 + c;
                 const bool in = k0 + k < K;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) v[s][h] = in && mine ? lds128(me.sm + at + act + k * 4 + h * 16) : make_uint4(0, 0, 0, 0);
+                for (int grp = 0; grp < GROUPS; ++grp) {
+                    const int j = grp * 8 + g / COLS;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        v[grp][s][h] = in && j < n && q < 3 ? lds128(stage + j * hrow<FR, W_BF16>() + k * 4 + h * 16) : make_uint4(0, 0, 0, 0);
+                }
 #pragma unroll
                 for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) a[s][i][h] = in ? lds128(row + at + (i * 16 + h * 8) * L::PITCH + k * 2) : make_uint4(0, 0, 0, 0);
             }
-            float sum[R][4] = {};
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                uint32_t w[8] = {v[s][0].x, v[s][0].y, v[s][0].z, v[s][0].w, v[s][1].x, v[s][1].y, v[s][1].z, v[s][1].w};
+            for (int grp = 0; grp < GROUPS; ++grp) {
+                float sum[SETS][R][4] = {};                     // short chains of products
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float r = __uint_as_float(w[e]) - __uint_as_float(w[e] & m1);
-                    w[e] = __float_as_uint(r - __uint_as_float(__float_as_uint(r) & m2));
+                for (int s = 0; s < STEPS; ++s) {
+                    const uint4 &lo = v[grp][s][0], &hi = v[grp][s][1];
+                    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    uint32_t p[8];
+#pragma unroll
+                    for (int set = 0; set < SETS; ++set) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            if (TOK == 2) p[e] = rest(rest(w[e], m1), m2);
+                            else p[e] = set == 0 ? w[e] : rest(p[e], up);
+                        }
+                        const uint32_t b0 = __byte_perm(p[0], p[1], 0x7632), b1 = __byte_perm(p[2], p[3], 0x7632);
+                        const uint32_t b2 = __byte_perm(p[4], p[5], 0x7632), b3 = __byte_perm(p[6], p[7], 0x7632);
+#pragma unroll
+                        for (int i = 0; i < R; ++i) {
+                            const uint4 &a0 = a[s][i][0], &a1 = a[s][i][1];
+                            mma_bf16(sum[set][i], a0.x, a1.x, a0.y, a1.y, b0, b1);
+                            mma_bf16(sum[set][i], a0.z, a1.z, a0.w, a1.w, b2, b3);
+                        }
+                    }
                 }
-                const uint32_t b0 = __byte_perm(w[0], w[1], 0x7632), b1 = __byte_perm(w[2], w[3], 0x7632);
-                const uint32_t b2 = __byte_perm(w[4], w[5], 0x7632), b3 = __byte_perm(w[6], w[7], 0x7632);
 #pragma unroll
-                for (int i = 0; i < R; ++i) {
-                    const uint4 &a0 = a[s][i][0], &a1 = a[s][i][1];
-                    mma_bf16(sum[i], a0.x, a1.x, a0.y, a1.y, b0, b1);
-                    mma_bf16(sum[i], a0.z, a1.z, a0.w, a1.w, b2, b3);
-                }
+                for (int i = 0; i < R; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[grp][i][e] += TOK == 2 ? sum[0][i][e] : add_parts(sum[0][i][e], sum[SETS > 1][i][e] + sum[SETS - 1][i][e]);
             }
-#pragma unroll
-            for (int i = 0; i < R; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][e] += sum[i][e];
         }
         release(me);
     }
-    // Columns 4 j, 4 j + 1 are in the lanes with lane % 4 = 2 j, column 4 j + 2 in the next ones
-    const int tok0 = __ffs(mask) - 1, tok1 = __ffs(mask & (mask - 1u)) - 1, quad = me.lane & ~3;
+    // A lane has columns 2 (lane % 4) and + 1, of the unit's tokens; t wants those of the layer's.
+    const int quad = me.lane & ~3;
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float low = acc[i][2 * h + 1] + __shfl_down_sync(0xffffffffu, acc[i][2 * h], 1);
-            const float all = add_parts(acc[i][2 * h], low);
-            const float y0 = __shfl_sync(0xffffffffu, all, quad), y1 = __shfl_sync(0xffffffffu, all, quad + 2);
+            float all = 0.f;                                    // two tokens: parts 0 and 1 here, part 2 in the next lane
+            if (TOK == 2) all = add_parts(acc[0][i][2 * h], acc[0][i][2 * h + 1] + __shfl_down_sync(0xffffffffu, acc[0][i][2 * h], 1));
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int tok = nt * 8 + (me.lane & 3) * 2 + e;
-                    t[i][nt * 4 + h * 2 + e] = tok == tok0 ? y0 : tok == tok1 ? y1 : 0.f;
+                    const int tok = nt * 8 + (me.lane & 3) * 2 + e, j = __popc(mask & ((1u << tok) - 1u));
+                    float y = 0.f;
+                    if (TOK == 2) {
+                        y = __shfl_sync(0xffffffffu, all, quad + (j * 2 & 3));
+                    } else {
+#pragma unroll
+                        for (int grp = 0; grp < GROUPS; ++grp)
+#pragma unroll
+                            for (int o = 0; o < 2; ++o) {
+                                const float z = __shfl_sync(0xffffffffu, acc[grp][i][2 * h + o], quad + (j >> 1 & 3));
+                                if (j >> 3 == grp && (j & 1) == o) y = z;
+                            }
+                    }
+                    t[i][nt * 4 + h * 2 + e] = (mask >> tok) & 1u ? y : 0.f;
                 }
         }
+}
+
+// The same for the shared experts of layers with 8-bit ones, which are few: called, as the others need the registers (four
+// tokens: e4m3 261 us instead of 266, block-scaled 282 instead of 286).
+template <int FR, int NT, int R>
+struct Called {
+    float t[R][NT * 4];
+    int slot;
+    uint32_t phase;
+};
+template <int FR, int NT, int R>
+__device__ __noinline__ Called<FR, NT, R> unit_parts_called(Me me, int K, uint32_t mask) {
+    Called<FR, NT, R> o;
+    unit_parts<FR, NT, R, NT * 8>(o.t, me, K, mask);
+    o.slot = me.ring.slot;
+    o.phase = me.ring.phase;
+    return o;
 }
 
 // One unit of 16 rows in fp32: lane pairs share a row, each lane every other 16-byte piece of the warp's
@@ -1263,8 +1281,24 @@ struct Kernel {
                     m[nt][j] = 0u;
                     if (F != W_BF16 && ((q.mask >> tok) & 1u)) m[nt][j] = __ldcg(p.hmax + row);
                 }
-            if (FR == W_BF16 && __popc(q.mask) <= 2) unit_parts<FR, NT, R>(t, me, K, q.mask);
-            else unit_mma<FR, F, NT, 2, R>(t, me, Stage<FR, R>::scales(p.T), K, q.mask);
+            if constexpr (F == W_BF16) {
+                if constexpr (FR != W_BF16) {
+                    const Called<FR, NT, R> o = unit_parts_called<FR, NT, R>(me, K, q.mask);
+#pragma unroll
+                    for (int i = 0; i < R; ++i)
+#pragma unroll
+                        for (int j = 0; j < NT * 4; ++j) t[i][j] = o.t[i][j];
+                    me.ring.slot = o.slot;
+                    me.ring.phase = o.phase;
+                } else {
+                    const int n = __popc(q.mask);
+                    if (n <= 2) unit_parts<FR, NT, R, 2>(t, me, K, q.mask);
+                    else if (n <= 8) unit_parts<FR, NT, R, 8>(t, me, K, q.mask);
+                    else unit_parts<FR, NT, R, NT * 8>(t, me, K, q.mask);
+                }
+            } else {
+                unit_mma<FR, F, NT, 2, R>(t, me, Stage<FR, R>::scales(p.T), K, q.mask);
+            }
 #pragma unroll
             for (int j = 0; j < NT * 4; ++j) {
                 const int tok = j / 4 * 8 + (me.lane & 3) * 2 + (j & 1);
