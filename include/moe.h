@@ -158,8 +158,9 @@ const char* moe_version(void);
  * 4 = token or slot index out of range).  The only call that synchronises. */
 moe_status_t moe_check_device_error(void* ws, size_t ws_bytes, moe_stream_t stream, uint32_t* detail);
 
-/* Clears the workspace's error word (asynchronously on `stream`).  Call once after
- * allocating a workspace; moe_check_device_error() also clears it. */
+/* Clears the workspace's error word, and the counts that the workspaces of moe_layer_forward_few, moe_grad_norm
+ * and moe_clip_grads keep beside it (asynchronously on `stream`: calls on other streams have to wait for it).
+ * Call once after allocating a workspace; moe_check_device_error() also clears the error word. */
 moe_status_t moe_ws_init(void* ws, size_t ws_bytes, moe_stream_t stream);
 
 /*
@@ -564,7 +565,10 @@ moe_status_t moe_clip_grads(const moe_tensor_t* grads, const moe_tensor_t* out, 
  * quantises them, by that quantisation.  Hidden values are fp32; for FP8 experts they are read with 22
  * significant bits, and a row of x or of hidden values is accurate to 2^-39 of its largest finite value, or
  * to 2^-151 where that is below 2^-112.
- * Sums are fp32, in an order that depends on sizes and picks alone.
+ * Sums are fp32, in an order that depends on sizes and picks alone (and is another one than moe_layer_forward's:
+ * of two keys that lie within rounding of each other, the two calls can pick another one).
+ * Which to call: this one up to 8 tokens, with FP8 experts up to 4, and always for MOE_F32; beyond that it still is
+ * faster for small layers, and moe_layer_forward for large ones (layers of 64 and 256 experts, one B200).
  * A pick that does not exist (NaN logits, or all other keys -infinity) sets error bit 1 and is left out.
  * Sizes: as the layer's, T <= MOE_FEW_MAX_TOKENS, d <= 32768, and for MOE_F32 d, inter and inter_shared
  * multiples of 4 (MOE_ERR_UNSUPPORTED otherwise); x, centroids, out and all matrices 16-byte aligned
