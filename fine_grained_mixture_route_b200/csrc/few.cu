@@ -398,8 +398,8 @@ __device__ __forceinline__ void unit_mma(float (&acc)[R][NT * 4], Me& me, int sf
 }
 
 // A unit of the down-projection with 16-bit weights and up to TOK tokens, t as unit_mma's.  Every fp32 number of h is the sum of
-// three bf16 ones, exactly: each part is the upper half of what the parts before leave, its top 8 bits.  (Of an infinite number or
-// NaN the first part is one too, and the others mean nothing.)  The unit's tokens stand in order in the products' columns, so
+// three bf16 ones, exactly (down to bf16's smallest step, 2^-133): each part is the upper half of what the parts before leave, its
+// top 8 bits.  (Of an infinite number or NaN the first part is one too, and the others mean nothing.)  The unit's tokens stand in order in the products' columns, so
 // that 9 to 16 tokens of the layer take a second group of columns only in units that have as many.  With one or two tokens, as most
 // units of routed experts have, the parts take the free columns: column 4 j + q is part q of token j, a third of the products;
 // else column j is token j and each part has products of its own.  (16 tokens, alternating inputs: 64 experts of 1408 x 2048
@@ -1441,7 +1441,7 @@ struct Kernel {
 
 template <int FR, int NT, int R>
 __global__ void __launch_bounds__(THREADS, 1) few_kernel(const __grid_constant__ Params p) {
-    extern __shared__ __align__(16) char sm[];
+    extern __shared__ __align__(128) char sm[];
     Kernel<FR, NT, R> k(p, sm);
     if (threadIdx.x == 0) {
         const uint32_t bars = smem_u32(sm + k.L.bars);
